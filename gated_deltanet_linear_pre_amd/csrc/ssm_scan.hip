@@ -36,6 +36,8 @@
 //   fp16: 2 parts (22 bits), scaled by a power of two to the largest value of
 //         the row or column that shares a contraction, as fp16's range asks;
 //   fp32: one part, on the fp32 matrix instructions.
+#include <type_traits>
+
 #include "ssm_device.h"
 #include "ssm_internal.h"
 
@@ -78,20 +80,43 @@ template <> struct Mat<float> {
     }
 };
 
-// v as a sum of PARTS operands
-template <typename TI, int PARTS>
-__device__ __forceinline__ void split(const float (&v)[8], typename Mat<TI>::frag (&out)[PARTS])
+// v = sum of PARTS values of the matrix type, each the nearest to what the
+// ones before it leave.  Two values at a time: their conversion and packing
+// are one instruction.
+template <typename T> struct Pair {
+    typedef T t2 __attribute__((ext_vector_type(2)));
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    static __device__ __forceinline__ t2 narrow(f2 v) { return __builtin_convertvector(v, t2); }
+    static __device__ __forceinline__ f2 widen(t2 v) { return f2{(float)v[0], (float)v[1]}; }
+};
+template <typename T, int PARTS, int NV>
+__device__ __forceinline__ void split(const float *v, T (*out)[NV])
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float r = v[i];
+    for (int i = 0; i < NV; i += 2) {
+        typename Pair<T>::f2 r = {v[i], v[i + 1]};
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
-            const TI h = (TI)r;
-            out[p][i] = h;
-            r -= (float)h;
+            const typename Pair<T>::t2 h = Pair<T>::narrow(r);
+            out[p][i] = h[0];
+            out[p][i + 1] = h[1];
+            if (p + 1 < PARTS) {
+                const typename Pair<T>::f2 w = Pair<T>::widen(h);
+                r[0] -= w[0];
+                r[1] -= w[1];
+            }
         }
     }
+}
+template <typename T, int PARTS>
+__device__ __forceinline__ void split8(const float (&v)[8], typename Mat<T>::frag (&out)[PARTS])
+{
+    T o[PARTS][8];
+    split<T, PARTS, 8>(v, o);
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[p][i] = o[p][i];
 }
 
 // 8 consecutive values of an LDS row
@@ -107,47 +132,111 @@ __device__ __forceinline__ Mat<float>::frag row8<float>(const float *p)
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Transposed operand: lane (g, r) gets rows row0 + 8g + 0..7 of one column,
-// column r of the 16 that the four column quads col(q) = 4 columns each make
-// up.  16-bit: two transposing reads, in which lane i of 16 addresses row i/4
-// and quad i%4 and receives column i of the 4 rows.
-template <typename T, typename Col>
-__device__ __forceinline__ typename Mat<T>::frag col8(const T *base, int pitch, int row0, int lane, Col col)
+// A 16-byte vector of a row of B (columns col..) to its places (see ScanShared)
+__device__ __forceinline__ void store_b(float *row, int col, Vec16<float>::type v)
+{
+    *reinterpret_cast<f4 *>(row + (col & ~31) + (col & 4) * 4 + (col & 24) / 2) = v;
+}
+template <typename T>
+__device__ __forceinline__ void store_b(T *row, int col, typename Vec16<T>::type v)
+{
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    T *p = row + (col & ~31) + (col & 24) / 2;
+    *reinterpret_cast<t4 *>(p) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+    *reinterpret_cast<t4 *>(p + 16) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+}
+// n = 32j + 8g + 0..7 of a permuted row of B
+template <typename T>
+__device__ __forceinline__ typename Mat<T>::frag rowb(const T *row, int j, int g)
+{
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    typedef t4 t4a __attribute__((aligned(8)));
+    const t4 a = *reinterpret_cast<const t4a *>(row + 32 * j + 4 * g), b = *reinterpret_cast<const t4a *>(row + 32 * j + 16 + 4 * g);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Transposed operand: lane (g, r) gets rows row0 + 8g + 0..7 of column
+// col0 + r.  16-bit: two transposing reads, in which lane i of 16
+// addresses row i/4 and columns 4(i%4).. and receives column i of the 4 rows.
+template <typename T>
+__device__ __forceinline__ typename Mat<T>::frag col8(const T *base, int pitch, int row0, int col0, int lane)
 {
     const int g = lane >> 4, c = lane & 15;
     typedef short s4 __attribute__((ext_vector_type(4)));
     typedef short s8 __attribute__((ext_vector_type(8)));
     typedef __attribute__((address_space(3))) s4 lds_s4;
-    const T *p = base + (row0 + 8 * g + (c >> 2)) * pitch + col(c & 3);
+    const T *p = base + (row0 + 8 * g + (c >> 2)) * pitch + col0 + 4 * (c & 3);
     const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(p));
     const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(p + 4 * pitch));
     return __builtin_bit_cast(typename Mat<T>::frag, (s8)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
-template <typename Col>
-__device__ __forceinline__ Mat<float>::frag col8(const float *base, int pitch, int row0, int lane, Col col)
+template <>
+__device__ __forceinline__ Mat<float>::frag col8<float>(const float *base, int pitch, int row0, int col0, int lane)
 {
     const int g = lane >> 4, c = lane & 15;
-    const float *p = base + (row0 + 8 * g) * pitch + col(c >> 2) + (c & 3);
+    const float *p = base + (row0 + 8 * g) * pitch + col0 + c;
     Mat<float>::frag v;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = p[i * pitch];
     return v;
 }
 
-// Power of two that brings `most` (>= 0) to 2^13..2^14, and its inverse:
-// products with it are exact.  Non-finite values stay so.
+// Power of two that brings `most` (>= 0) to 2^13..2^14, at most 2^40 (smaller
+// values than 2^-26 keep an error of 2^-65), and its inverse: products with
+// it are exact.  Non-finite values stay so.
 __device__ __forceinline__ void scale_of(float most, float &up, float &down)
 {
     int k = 14 - __builtin_amdgcn_frexp_expf(most);
-    k = k < -100 ? -100 : k > 100 ? 100 : k;
+    k = k < -100 ? -100 : k > 40 ? 40 : k;
     up = __int_as_float((127 + k) << 23);
     down = __int_as_float((127 - k) << 23);
 }
-// the largest of the four lanes that share lane & 15
+// the largest of the four lanes that share lane & 15 (x >= 0): a lane-half
+// swap of x with itself leaves the two halves' values side by side, and a
+// swap of 16-lane rows likewise
 __device__ __forceinline__ float max_of_groups(float x)
 {
-    x = fmaxf(x, __shfl_xor(x, 16, 64));
-    return fmaxf(x, __shfl_xor(x, 32, 64));
+    const unsigned u = __float_as_uint(x);
+    const auto h = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const unsigned v = __float_as_uint(fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1])));
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// ---- 64-bit values across lanes ---------------------------------------------
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp64(double x)  // 0 where the source lane or the row is left out
+{
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, x);
+    const unsigned lo = __builtin_amdgcn_update_dpp(0, (int)(unsigned)u, CTRL, ROWS, 0xF, false);
+    const unsigned hi = __builtin_amdgcn_update_dpp(0, (int)(unsigned)(u >> 32), CTRL, ROWS, 0xF, false);
+    return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+// Sum of the lanes up to this one, over runs of W (32 or 64) lanes: shifts by
+// 1, 2, 4, 8 inside the rows of 16, then the last lane of the row before, then
+// that of the half before
+template <int W>
+__device__ __forceinline__ double scan64(double x)
+{
+    x += dpp64<0x111, 0xF>(x);
+    x += dpp64<0x112, 0xF>(x);
+    x += dpp64<0x114, 0xF>(x);
+    x += dpp64<0x118, 0xF>(x);
+    x += dpp64<0x142, 0xA>(x);
+    if (W == 64) x += dpp64<0x143, 0xC>(x);
+    return x;
+}
+// lane `at` of this lane's run of W lanes
+template <int W>
+__device__ __forceinline__ double lane64(double x, int at, int lane)
+{
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, x);
+    auto pick = [&](int l) {
+        const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)u, l);
+        const unsigned hi = __builtin_amdgcn_readlane((int)(unsigned)(u >> 32), l);
+        return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+    };
+    return W == 64 || lane < 32 ? pick(at) : pick(at + 32);
 }
 
 // Barrier that orders LDS only: global loads and stores in flight stay so.
@@ -161,18 +250,27 @@ __device__ __forceinline__ void lds_sync()
 
 constexpr int BATCH = 256;  // tokens whose decays are formed at a time, one a thread
 
+// Rows of B are permuted: the 32 values n = 32j + 8q + 4a + i stand at
+// 32j + 16a + 4q + i, so that the 16 columns of a state tile (j, a) are
+// consecutive for the transposing reads, and 40 bytes longer than N (a row
+// read takes two 8-byte halves: 16 rows then start in 16 different bank pairs).
+// Rows of C and X are 32 bytes longer, those of M (also written in 8-byte
+// columns) 16.  Measured in cycles of an instruction, 4 waves reading: 16-byte
+// row reads 4.1 at 32 bytes, 8.1 at 16; transposing reads 4.1; 8-byte ones 4.8.
 template <typename TI, int N, int PARTS, bool OUT> struct __attribute__((aligned(16))) ScanShared {
-    static constexpr int Q = Mat<TI>::Q, PAD = 16 / sizeof(TI);
-    static constexpr int NP = N + PAD, XP = 64 + PAD, MP = Q + PAD;
-    TI B[Q][NP];
+    static constexpr int Q = Mat<TI>::Q, E16 = 16 / sizeof(TI), REFS = Q / 16 - 1;
+    static constexpr int BP = N + 40 / sizeof(TI), CP = N + 2 * E16, XP = 64 + 2 * E16, MP = Q + E16;
+    TI C[OUT ? Q : 1][CP];
     TI X[Q][XP];
-    TI C[OUT ? Q : 1][NP];
     TI M[OUT ? PARTS : 1][OUT ? Q : 1][MP];
-    float2 lam[BATCH];           // L_t in two floats
-    float dt[BATCH], E[BATCH];   // dt_t, exp(L_t)
-    float W[BATCH];              // exp(L_Q - L_t) dt_t
+    TI B[Q][BP];
+    float2 lam[OUT ? BATCH : 1];                       // L_t in two floats
+    float dt[OUT ? BATCH : 1], E[OUT ? BATCH : 1];     // dt_t, exp(L_t)
+    float W[BATCH];              // exp(L_end - L_t) dt_t, to the end of the chunk (without outputs: of the batch)
+    float F[OUT ? BATCH : 1];    // exp(L_t - L_r), r the first token of t's tile of 16
+    float G[REFS][OUT ? BATCH : 1];  // exp(L_r - L_t) dt_t, r the first token of a later tile
     float alpha[BATCH / Q];      // exp(L_Q)
-    double total[BATCH / Q];     // L_Q
+    double total[4];             // log decay of a wave's 64 tokens (without outputs)
     float mscale[Q];             // fp16: 1 / scale of M's row t
 };
 
@@ -198,8 +296,9 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
     constexpr int Q = MT::Q, SP = MT::STATE_PARTS, J = N / 32, TT = Q / 16, KK = Q / 32;
     constexpr int V = Vec16<TI>::n;
     typedef typename Vec16<TI>::type vec;
-    constexpr int NB = Q * N / V / 256 > 0 ? Q * N / V / 256 : 1;  // vectors of B (and C) a thread moves
+    constexpr int NB = Q * N / V / 256;  // vectors of B (and C) a thread moves
     constexpr int NX = Q * 64 / V / 256;
+    constexpr bool DIRECT = !OUT && !MT::scaled && N <= 128;  // products accumulate onto S itself
     __shared__ Shared sh;
 
     SeqTile st;
@@ -212,7 +311,8 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
     const int pt_n = (d.P + 63) / 64;
     const int h = blockIdx.x / pt_n, pt = blockIdx.x - h * pt_n;
     const int grp = h / d.hg;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, c = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int p0 = pt * 64 + w * 16;      // of this wave
     const bool mine = p0 < d.P;           // (a wave past P only helps with loads and M)
     const int cols = d.P - pt * 64 < 64 ? d.P - pt * 64 : 64;
@@ -222,10 +322,50 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
     const TI *dtp = static_cast<const TI *>(a.dt) + (int64_t)(st.begin + first) * d.dt_stride + h;
     const int xc = h * d.P + pt * 64, bc = d.H * d.P + grp * N, cc = bc + d.G * N;
 
-    // ---- state: lane (g, p = c), n = 32j + 8g + 4a + i
+    // ---- state: lane (g, p = c), n = 32j + 8g + 4a + i.  fp16: S stands
+    // for S * sdown, a power of two of row p that the last chunk's products needed.
     f4 S[J][2];
+    float sdown = 1.f;
     const int64_t head_at = ((int64_t)h * d.P + p0 + c) * N + 8 * g;
     const int64_t seq_size = (int64_t)d.H * d.P * N;
+    const float neg_a = -expf(a.A_log[h]), dt_bias = a.dt_bias[h], Dh = OUT && a.D ? a.D[h] : 0.f;
+    double total = 0.0;       // log decay of the segment (without outputs)
+    float batch_alpha = 1.f;  // decay of a batch
+
+    // ---- rows of a chunk in registers: vector i of a thread is row
+    // i*RB + tid / (N/V) of B and C, i*RX + tid / (64/V) of X
+    constexpr int RB = 256 * V / N, RX = 256 * V / 64;
+    vec rB[NB], rC[OUT ? NB : 1], rX[NX];
+    const int brow = tid / (N / V), bcol = tid % (N / V) * V, xr = tid / (64 / V), xcol = tid % (64 / V) * V;
+    // (byte offsets of 32 bits beside a uniform base: one register for all rows)
+    const uint32_t ob = ((uint32_t)brow * d.C + bcol) * sizeof(TI);
+    const uint32_t ox = ((uint32_t)xr * d.C + (xcol < cols ? xcol : 0)) * sizeof(TI);
+    const uint32_t oy = ((uint32_t)c * d.H * d.P + 4 * g) * sizeof(TO);
+    auto at = [](const TI *base, uint32_t bytes) { return ld16(reinterpret_cast<const TI *>(reinterpret_cast<const char *>(base) + bytes)); };
+    auto fetch = [&](int t0) {
+        const TI *base = xrow + (int64_t)t0 * d.C;
+        if (t0 + Q <= n_tok) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                rB[i] = at(base + bc + (int64_t)i * RB * d.C, ob);
+                if (OUT) rC[i] = at(base + cc + (int64_t)i * RB * d.C, ob);
+            }
+#pragma unroll
+            for (int i = 0; i < NX; ++i) rX[i] = at(base + xc + (int64_t)i * RX * d.C, ox);
+        } else {  // rows past the end are zero
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const bool in = t0 + i * RB + brow < n_tok;
+                rB[i] = in ? at(base + bc + (int64_t)i * RB * d.C, ob) : vec(TI(0));
+                if (OUT) rC[i] = in ? at(base + cc + (int64_t)i * RB * d.C, ob) : vec(TI(0));
+            }
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+                rX[i] = t0 + i * RX + xr < n_tok ? at(base + xc + (int64_t)i * RX * d.C, ox) : vec(TI(0));
+        }
+    };
+    TI raw = tid < n_tok ? dtp[tid * d.dt_stride] : TI(0);
+    fetch(0);
     const float *S0 = nullptr;
     if (OUT && mine) {
         if (!single) S0 = a.seg_state + slot * seq_size + head_at;
@@ -237,29 +377,81 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
         for (int q = 0; q < 2; ++q)
             S[j][q] = S0 ? *reinterpret_cast<const f4 *>(S0 + 32 * j + 4 * q) : f4(0.f);
 
-    const float neg_a = -expf(a.A_log[h]), dt_bias = a.dt_bias[h], Dh = OUT && a.D ? a.D[h] : 0.f;
-    double total = 0.0;  // log decay of the segment
+    // M's t tile of a wave: the two blocks that usually share a CU take them
+    // in opposite order (tile t costs t + 1 products)
+    const int mt = TT == 4 && (((int64_t)slot * gridDim.x + blockIdx.x) >> 8 & 1) ? 3 - w : w;
 
-    // ---- rows of the next chunk, in registers (zero past the end)
-    vec rB[NB], rC[OUT ? NB : 1], rX[NX];
-    auto fetch = [&](int t0) {
+    // ---- M's rows t of tile T: D = B C^T has rows s, lane (g, t = c)
+    auto form_m = [&](auto tile, int bt) {
+        constexpr int T = decltype(tile)::value;
+        frag cf[J], bf[T + 1][J];
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const int at = i * 256 + tid, row = at / (N / V), col = at % (N / V) * V;
-            const bool in = row < Q && t0 + row < n_tok;
-            const TI *p = xrow + (int64_t)(t0 + row) * d.C + col;
-            rB[i] = in ? ld16(p + bc) : vec(TI(0));
-            if (OUT) rC[i] = in ? ld16(p + cc) : vec(TI(0));
+        for (int j = 0; j < J; ++j) {
+            cf[j] = row8(&sh.C[16 * T + c][32 * j + 8 * g]);
+#pragma unroll
+            for (int s = 0; s <= T; ++s) bf[s][j] = rowb(&sh.B[16 * s + c][0], j, g);
+        }
+        const float2 lt = sh.lam[bt + 16 * T + c];
+        const float Ft = sh.F[bt + 16 * T + c];
+        float2 ls[4];
+        float ds[4];
+        f4 Gs[T > 0 ? T : 1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ls[i] = sh.lam[bt + 16 * T + 4 * g + i];
+            ds[i] = sh.dt[bt + 16 * T + 4 * g + i];
         }
 #pragma unroll
-        for (int i = 0; i < NX; ++i) {
-            const int at = i * 256 + tid, row = at / (64 / V), col = at % (64 / V) * V;
-            const bool in = t0 + row < n_tok && col < cols;
-            rX[i] = in ? ld16(xrow + (int64_t)(t0 + row) * d.C + xc + col) : vec(TI(0));
+        for (int s = 0; s < T; ++s) Gs[s] = *reinterpret_cast<const f4 *>(&sh.G[T > 0 ? T - 1 : 0][bt + 16 * s + 4 * g]);
+        __builtin_amdgcn_sched_barrier(0);
+        f4 dd[T + 1];
+#pragma unroll
+        for (int s = 0; s <= T; ++s) dd[s] = f4(0.f);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int s = 0; s <= T; ++s) dd[s] = MT::mma(bf[s][j], cf[j], dd[s]);
+        float most = 0.f;
+#pragma unroll
+        for (int s = 0; s < T; ++s) dd[s] = dd[s] * Gs[s] * Ft;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int si = 4 * g + i;
+            const float v = dd[T][i] * (exp_fast((lt.x - ls[i].x) + (lt.y - ls[i].y)) * ds[i]);
+            dd[T][i] = si < c ? v : si == c ? v + Dh : 0.f;
         }
+        if (MT::scaled) {
+#pragma unroll
+            for (int s = 0; s <= T; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) most = fmaxf(most, fabsf(dd[s][i]));
+            float up, down;
+            scale_of(max_of_groups(most), up, down);
+            if (g == 0) sh.mscale[16 * T + c] = down;
+#pragma unroll
+            for (int s = 0; s <= T; ++s) dd[s] *= up;
+        }
+#pragma unroll
+        for (int s = 0; s <= T; ++s) {
+            typedef TI t4 __attribute__((ext_vector_type(4)));
+            const float v[4] = {dd[s][0], dd[s][1], dd[s][2], dd[s][3]};
+            TI o[PARTS][4];
+            split<TI, PARTS, 4>(v, o);
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) {
+                const t4 q = {o[p][0], o[p][1], o[p][2], o[p][3]};
+                *reinterpret_cast<t4 *>(&sh.M[p][16 * T + c][16 * s + 4 * g]) = q;
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
     };
-    fetch(0);
-    TI raw = tid < n_tok ? dtp[tid * d.dt_stride] : TI(0);
+    if (OUT) {  // the tiles of M above the diagonal that a 32-deep product touches
+        typedef TI t4 __attribute__((ext_vector_type(4)));
+        if (w < KK)
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p)
+                *reinterpret_cast<t4 *>(&sh.M[p][32 * w + c][32 * w + 16 + 4 * g]) = t4(TI(0));
+    }
 
     for (int t0 = 0; t0 < n_tok; t0 += Q) {
         if (t0) lds_sync();  // every wave is done with the last chunk
@@ -270,161 +462,191 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
             const bool in = t0 + tid < n_tok;
             float dt = 0.f, lam = 0.f;
             if (in) step_size((float)raw, dt_bias, neg_a, d.dt_min, d.dt_max, dt, lam);
-            double L = lam;
+            constexpr int QS = OUT ? Q : 64;  // (without outputs only the batch's end matters)
+            const double L = scan64<QS>(lam);
+            double LQ = lane64<QS>(L, QS - 1, lane);
+            if (OUT) {
+                const float hi = (float)L;
+                sh.lam[tid] = make_float2(hi, (float)(L - (double)hi));
+                sh.dt[tid] = dt;
+                sh.E[tid] = exp_fast(hi);
+                const int place = lane & (Q - 1);
+                double first_of_tile = lane64<Q>(L, 0, lane);
 #pragma unroll
-            for (int m = 1; m < Q; m <<= 1) {
-                const double o = __shfl_up(L, m, Q);
-                if ((lane & (Q - 1)) >= m) L += o;
+                for (int r = 1; r < TT; ++r) {
+                    const double Lr = lane64<Q>(L, 16 * r, lane);
+                    if (place >= 16 * r) first_of_tile = Lr;
+                    sh.G[r - 1][tid] = place < 16 * r ? exp_fast((float)(Lr - L)) * dt : 0.f;
+                }
+                sh.F[tid] = exp_fast((float)(L - first_of_tile));
+                if (place == 0) sh.alpha[tid / Q] = exp_fast((float)LQ);
+            } else {
+                if (lane == 0) sh.total[w] = LQ;
+                lds_sync();
+                double all = 0.0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const double o = sh.total[i];
+                    all += o;
+                    if (i > w) LQ += o;
+                }
+                batch_alpha = exp_fast((float)all);
+                total += all;
             }
-            const double LQ = __shfl(L, Q - 1, Q);
-            const float hi = (float)L;
-            sh.lam[tid] = make_float2(hi, (float)(L - (double)hi));
-            sh.dt[tid] = dt;
-            sh.E[tid] = expf(hi);
-            sh.W[tid] = expf((float)(LQ - L)) * dt;
-            if ((lane & (Q - 1)) == 0) {
-                sh.alpha[tid / Q] = expf((float)LQ);
-                sh.total[tid / Q] = LQ;
-            }
+            sh.W[tid] = exp_fast((float)(LQ - L)) * dt;
             const int nt = t0 + BATCH + tid;
             raw = nt < n_tok ? dtp[nt * d.dt_stride] : TI(0);
         }
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            const int at = i * 256 + tid, row = at / (N / V), col = at % (N / V) * V;
-            if (row < Q) {
-                st16(&sh.B[row][col], rB[i]);
-                if (OUT) st16(&sh.C[row][col], rC[i]);
-            }
+            store_b(&sh.B[i * RB + brow][0], bcol, rB[i]);
+            if (OUT) st16(&sh.C[i * RB + brow][bcol], rC[i]);
         }
 #pragma unroll
-        for (int i = 0; i < NX; ++i) {
-            const int at = i * 256 + tid, row = at / (64 / V), col = at % (64 / V) * V;
-            st16(&sh.X[row][col], rX[i]);
-        }
-        if (t0 + Q < n_tok) fetch(t0 + Q);
+        for (int i = 0; i < NX; ++i) st16(&sh.X[i * RX + xr][xcol], rX[i]);
         lds_sync();
+        if (!OUT) fetch(t0 + Q);
 
         const int rows = n_tok - t0 < Q ? n_tok - t0 : Q;  // (the others are zero)
         // Each product below loads all its operands from LDS, then issues its
         // matrix instructions, and its results are taken before the next
         // product's loads: no load is given registers of an operand in use.
-        if (OUT && w < TT) {
-            // ---- M's rows t of tile w: D = B C^T has rows s, lane (g, t = c)
-            frag cf[J], bf[TT][J];
-#pragma unroll
-            for (int j = 0; j < J; ++j) cf[j] = row8(&sh.C[16 * w + c][32 * j + 8 * g]);
-#pragma unroll
-            for (int s = 0; s < TT; ++s)
-#pragma unroll
-                for (int j = 0; j < J; ++j) bf[s][j] = row8(&sh.B[16 * s + c][32 * j + 8 * g]);
-            const float2 lt = sh.lam[bt + 16 * w + c];
-            float2 ls[TT][4];
-            float ds[TT][4];
-#pragma unroll
-            for (int s = 0; s < TT; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    ls[s][i] = sh.lam[bt + 16 * s + 4 * g + i];
-                    ds[s][i] = sh.dt[bt + 16 * s + 4 * g + i];
-                }
-            __builtin_amdgcn_sched_barrier(0);
-            f4 dd[TT];
-#pragma unroll
-            for (int s = 0; s < TT; ++s) dd[s] = f4(0.f);
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int s = 0; s < TT; ++s) dd[s] = MT::mma(bf[s][j], cf[j], dd[s]);
-            float m[TT][4], most = 0.f;
-#pragma unroll
-            for (int s = 0; s < TT; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int si = 16 * s + 4 * g + i, ti = 16 * w + c;
-                    const float e = exp_fast((lt.x - ls[s][i].x) + (lt.y - ls[s][i].y)) * ds[s][i];
-                    float v = si <= ti ? dd[s][i] * e : 0.f;
-                    if (si == ti) v += Dh;
-                    m[s][i] = v;
-                    most = fmaxf(most, fabsf(v));
-                }
-            float up = 1.f, down = 1.f;
-            if (MT::scaled) {
-                scale_of(max_of_groups(most), up, down);
-                if (g == 0) sh.mscale[16 * w + c] = down;
-            }
-#pragma unroll
-            for (int s = 0; s < TT; ++s) {
-                TI o[PARTS][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float r = MT::scaled ? m[s][i] * up : m[s][i];
-#pragma unroll
-                    for (int p = 0; p < PARTS; ++p) {
-                        o[p][i] = (TI)r;
-                        r -= (float)o[p][i];
-                    }
-                }
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p) {
-                    typedef TI t4 __attribute__((ext_vector_type(4)));
-                    const t4 v = {o[p][0], o[p][1], o[p][2], o[p][3]};
-                    *reinterpret_cast<t4 *>(&sh.M[p][16 * w + c][16 * s + 4 * g]) = v;
-                }
-            }
-        }
-
-        // ---- y^T = S C^T: rows p, lane (g, t = c); then exp(L_t)
         f4 acc[TT];
-        if (OUT && mine) {
-            frag cf[J][TT];
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int t = 0; t < TT; ++t) cf[j][t] = row8(&sh.C[16 * t + c][32 * j + 8 * g]);
-            float e[TT];
-#pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                acc[t] = f4(0.f);
-                e[t] = sh.E[bt + 16 * t + c];
+        if (OUT) {
+            if (mt == 0) form_m(std::integral_constant<int, 0>{}, bt);
+            else if (mt == 1) form_m(std::integral_constant<int, 1>{}, bt);
+            else if (TT > 2) {
+                if (mt == 2) form_m(std::integral_constant<int, (TT > 2 ? 2 : 0)>{}, bt);
+                else form_m(std::integral_constant<int, (TT > 2 ? 3 : 0)>{}, bt);
             }
-            float sup = 1.f, sdown = 1.f, rdown[4] = {1.f, 1.f, 1.f, 1.f};
-            if (MT::scaled) {
-                float most = 0.f;
+            if (mine) {
+                // ---- y^T = S C^T: rows p, lane (g, t = c); then exp(L_t)
+                frag cf[J][TT];
 #pragma unroll
                 for (int j = 0; j < J; ++j)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(S[j][i >> 2][i & 3]));
-                scale_of(max_of_groups(most), sup, sdown);  // of row p = c
+                    for (int t = 0; t < TT; ++t) cf[j][t] = row8(&sh.C[16 * t + c][32 * j + 8 * g]);
+                float e[TT];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) rdown[i] = __shfl(sdown, 4 * g + i, 64);
+                for (int t = 0; t < TT; ++t) {
+                    acc[t] = f4(0.f);
+                    e[t] = sh.E[bt + 16 * t + c];
+                }
+                float up = 1.f, down = 1.f, rdown[4] = {1.f, 1.f, 1.f, 1.f};
+                if (MT::scaled) {
+                    float most = 0.f;
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(S[j][i >> 2][i & 3]));
+                    scale_of(max_of_groups(most), up, down);  // of row p = c
+                    down *= sdown;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) rdown[i] = __shfl(down, 4 * g + i, 64);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = MT::scaled ? S[j][i >> 2][i & 3] * up : S[j][i >> 2][i & 3];
+                    frag sp[PARTS];
+                    split8<TI, PARTS>(v, sp);
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                        for (int t = 0; t < TT; ++t) acc[t] = MT::mma(sp[p], cf[j][t], acc[t]);
+                }
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[t][i] *= MT::scaled ? e[t] * rdown[i] : e[t];
+                __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = MT::scaled ? S[j][i >> 2][i & 3] * sup : S[j][i >> 2][i & 3];
-                frag sp[PARTS];
-                split<TI, PARTS>(v, sp);
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-                    for (int t = 0; t < TT; ++t) acc[t] = MT::mma(sp[p], cf[j][t], acc[t]);
-            }
-#pragma unroll
-            for (int t = 0; t < TT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[t][i] *= MT::scaled ? e[t] * rdown[i] : e[t];
-            __builtin_amdgcn_sched_barrier(0);
         }
-
-        if (OUT) lds_sync();  // M is complete
+        if (OUT) fetch(t0 + Q);  // (past the end: zeros; without a branch, as the old values would live on beside it)
+        frag xf[KK];
         if (mine) {
-            frag xf[KK];
 #pragma unroll
-            for (int k = 0; k < KK; ++k) xf[k] = col8(&sh.X[0][0], Shared::XP, 32 * k, lane, [&](int q) { return 16 * w + 4 * q; });
-            if (OUT) {
+            for (int k = 0; k < KK; ++k) xf[k] = col8(&sh.X[0][0], Shared::XP, 32 * k, 16 * w, lane);
+            // ---- S <- alpha S + B^T (W x)
+            if (!OUT || t0 + Q < n_tok || (single && a.state_out)) {
+                float wt[KK][8];
+                float alpha = OUT ? sh.alpha[bt / Q] : bt ? 1.f : batch_alpha;
+#pragma unroll
+                for (int k = 0; k < KK; ++k)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) wt[k][i] = sh.W[bt + 32 * k + 8 * g + i];
+                float u[KK][8];
+#pragma unroll
+                for (int k = 0; k < KK; ++k)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[k][i] = (float)xf[k][i] * wt[k][i];
+                if (MT::scaled) {
+                    float most = 0.f, up;
+#pragma unroll
+                    for (int k = 0; k < KK; ++k)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(u[k][i]));
+                    alpha *= sdown;
+                    scale_of(max_of_groups(most), up, sdown);
+                    alpha *= up;
+#pragma unroll
+                    for (int k = 0; k < KK; ++k)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) u[k][i] *= up;
+                }
+                if (DIRECT && bt == 0) {
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) S[j][q] *= alpha;
+                }
+                frag uf[KK][SP];
+#pragma unroll
+                for (int k = 0; k < KK; ++k) split8<TI, SP>(u[k], uf[k]);
+                __builtin_amdgcn_sched_barrier(0);
+                // (in two parts of n, which bounds the registers: at N = 128 all
+                // of B^T at once spilled some, and 430 us on the packed batch
+                // of 27135 tokens became 490)
+                constexpr int JS = DIRECT || J < 2 ? J : J / 2;
+#pragma unroll
+                for (int j0 = 0; j0 < J; j0 += JS) {
+                    frag bf[JS][2][KK];
+#pragma unroll
+                    for (int j = 0; j < JS; ++j)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+#pragma unroll
+                            for (int k = 0; k < KK; ++k)
+                                bf[j][q][k] = col8(&sh.B[0][0], Shared::BP, 32 * k, 32 * (j0 + j) + 16 * q, lane);
+                    __builtin_amdgcn_sched_barrier(0);
+                    f4 z[JS][2];
+                    if (DIRECT) {
+#pragma unroll
+                        for (int j = 0; j < JS; ++j)
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) z[j][q] = S[j0 + j][q];
+                    }
+#pragma unroll
+                    for (int k = 0; k < KK; ++k)
+#pragma unroll
+                        for (int p = 0; p < SP; ++p)
+#pragma unroll
+                            for (int j = 0; j < JS; ++j)
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) z[j][q] = MT::mma(bf[j][q][k], uf[k][p], k + p || DIRECT ? z[j][q] : f4(0.f));
+#pragma unroll
+                    for (int j = 0; j < JS; ++j)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) S[j0 + j][q] = DIRECT ? z[j][q] : S[j0 + j][q] * alpha + z[j][q];
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+        if (OUT) {
+            lds_sync();  // M is complete
+            if (mine) {
                 // ---- y^T += x^T M^T, and out
                 frag mf[PARTS][TT][KK];
                 float md[TT];
@@ -439,97 +661,45 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
                         }
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                if (MT::scaled) {
+                f4 z[TT];
 #pragma unroll
-                    for (int t = 0; t < TT; ++t) acc[t] *= 1.0f / md[t];  // (a power of two: exact)
-                }
+                for (int t = 0; t < TT; ++t) z[t] = MT::scaled ? f4(0.f) : acc[t];
 #pragma unroll
                 for (int k = 0; k < KK; ++k)
 #pragma unroll
                     for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-                        for (int t = 2 * k; t < TT; ++t) acc[t] = MT::mma(xf[k], mf[p][t][k], acc[t]);
-                TO *yp = static_cast<TO *>(a.y) + ((int64_t)(st.begin + first + t0) * d.H + h) * d.P + p0 + 4 * g;
+                        for (int t = 2 * k; t < TT; ++t) z[t] = MT::mma(xf[k], mf[p][t][k], z[t]);
+                char *yp = reinterpret_cast<char *>(static_cast<TO *>(a.y) + ((int64_t)(st.begin + first + t0) * d.H + h) * d.P + p0);
                 typedef TO o4 __attribute__((ext_vector_type(4)));
                 o4 o[TT];
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
-                    const f4 v = MT::scaled ? acc[t] * md[t] : acc[t];
+                    const f4 v = MT::scaled ? z[t] * md[t] + acc[t] : z[t];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[t][i] = (TO)v[i];
                     __asm__ volatile("" : "+v"(o[t]));  // (taken here, not where it is stored)
                 }
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
-                    if (16 * t + c < rows) *reinterpret_cast<o4 *>(yp + (int64_t)(16 * t + c) * d.H * d.P) = o[t];
+                    if (16 * t + c < rows) *reinterpret_cast<o4 *>(yp + (int64_t)t * 16 * d.H * d.P * sizeof(TO) + oy) = o[t];
                 __builtin_amdgcn_sched_barrier(0);
-            }
-            // ---- S <- alpha S + B^T (W x)
-            if (!OUT || t0 + Q < n_tok || (single && a.state_out)) {
-                frag bf[J][2][KK];
-                float wt[KK][8];
-                const float alpha = sh.alpha[bt / Q];
-#pragma unroll
-                for (int k = 0; k < KK; ++k)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) wt[k][i] = sh.W[bt + 32 * k + 8 * g + i];
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int k = 0; k < KK; ++k)
-                            bf[j][q][k] = col8(&sh.B[0][0], Shared::NP, 32 * k, lane, [&](int r) { return 32 * j + 8 * r + 4 * q; });
-                float u[KK][8], most = 0.f;
-#pragma unroll
-                for (int k = 0; k < KK; ++k)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        u[k][i] = (float)xf[k][i] * wt[k][i];
-                        most = fmaxf(most, fabsf(u[k][i]));
-                    }
-                float up = 1.f, down = 1.f;
-                if (MT::scaled) {
-                    scale_of(max_of_groups(most), up, down);
-#pragma unroll
-                    for (int k = 0; k < KK; ++k)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) u[k][i] *= up;
-                }
-                frag uf[KK][SP];
-#pragma unroll
-                for (int k = 0; k < KK; ++k) split<TI, SP>(u[k], uf[k]);
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        f4 z = MT::scaled ? f4(0.f) : S[j][q] * alpha;
-#pragma unroll
-                        for (int k = 0; k < KK; ++k)
-#pragma unroll
-                            for (int p = 0; p < SP; ++p) z = MT::mma(bf[j][q][k], uf[k][p], z);
-                        if (MT::scaled) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) S[j][q][i] = fmaf(z[i], down, alpha * S[j][q][i]);
-                        } else {
-                            S[j][q] = z;
-                        }
-                    }
             }
         }
-        if (!OUT) total += sh.total[bt / Q];
     }
 
     if (!mine) return;
+    int lane_end = threadIdx.x & 63;
+    __asm__ volatile("" : "+v"(lane_end));  // (the state's address is formed again, not kept)
+    const int64_t end_at = ((int64_t)h * d.P + p0 + (lane_end & 15)) * N + 8 * (lane_end >> 4);
     float *to = nullptr;
-    if (!OUT) to = a.seg_state + slot * seq_size + head_at;
-    else if (single && a.state_out) to = a.state_out + st.n * seq_size + head_at;
+    if (!OUT) to = a.seg_state + slot * seq_size + end_at;
+    else if (single && a.state_out) to = a.state_out + st.n * seq_size + end_at;
     if (to) {
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) *reinterpret_cast<f4 *>(to + 32 * j + 4 * q) = S[j][q];
+            for (int q = 0; q < 2; ++q) *reinterpret_cast<f4 *>(to + 32 * j + 4 * q) = MT::scaled ? S[j][q] * sdown : S[j][q];
     }
     if (!OUT && tid == 0 && pt == 0) a.seg_decay[slot * d.H + h] = expf((float)total);
 }
@@ -551,23 +721,38 @@ __global__ __launch_bounds__(256) void ssm_segment_kernel(SsmDims d, ScanArgsT a
     f4 S = a.state ? *reinterpret_cast<const f4 *>(a.state + n * seq_size + at) : f4(0.f);
     float *p = a.seg_state + slot0 * seq_size + at;
     const float *dec = a.seg_decay + slot0 * d.H + h;
-    for (int s = 0; s < segs; ++s) {
-        const f4 own = *reinterpret_cast<const f4 *>(p + s * seq_size);
-        *reinterpret_cast<f4 *>(p + s * seq_size) = S;
-        S = S * dec[(int64_t)s * d.H] + own;
+    constexpr int AHEAD = 8;  // loads in flight: the stores would otherwise hold each one back
+    for (int s0 = 0; s0 < segs; s0 += AHEAD) {
+        f4 own[AHEAD];
+        float decay[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int64_t s = s0 + i < segs ? s0 + i : segs - 1;
+            own[i] = *reinterpret_cast<const f4 *>(p + s * seq_size);
+            decay[i] = dec[s * d.H];
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (s0 + i < segs) {
+                *reinterpret_cast<f4 *>(p + (s0 + i) * seq_size) = S;
+                S = S * decay[i] + own[i];
+            }
     }
     if (a.state_out) *reinterpret_cast<f4 *>(a.state_out + n * seq_size + at) = S;
 }
 
-// Tokens of a segment: as many as give the launch about SEG_BLOCKS blocks (two
-// on each of the 256 CUs), in whole batches of decays.
-constexpr int SEG_BLOCKS = 512;
+// Tokens of a segment, in whole batches of decays: as many as make the launch
+// about as many blocks as the chip's 256 CUs hold at once, two a CU, or one
+// with N = 256, whose LDS and registers leave room for one.  Measured: 2048
+// tokens of 64 heads, N = 128, bf16: 256 blocks 50 us, 512 45, 1024 44;
+// 27135 packed tokens: 530, 398, 420; N = 256, 2005 tokens of 32 heads of 128:
+// 256 blocks 100 us, 512 119.
 int segment_tokens(const SsmDims &d)
 {
-    const int64_t blocks = (int64_t)d.H * ((d.P + 63) / 64);
-    int64_t tile = (d.T * blocks + SEG_BLOCKS - 1) / SEG_BLOCKS;
+    const int64_t blocks = (int64_t)d.H * ((d.P + 63) / 64), room = d.N == 256 ? 256 : 512;
+    int64_t tile = (d.T * blocks + room - 1) / room;
     tile = (tile + BATCH - 1) / BATCH * BATCH;
-    return (int)(tile < BATCH ? BATCH : tile > (1 << 27) ? 1 << 27 : tile);
+    return (int)(tile < BATCH ? BATCH : tile);
 }
 
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
