@@ -6,7 +6,7 @@
 //
 // gfx950 mapping.  One read and one write of an element for about 2K+5 flop:
 // bound by HBM bandwidth.  A lane owns one 16-byte vector of channels (8 of 16
-// bits, 4 of fp32) and CONV_RUN consecutive tokens, so every memory
+// bits, 4 of fp32) and a run of 4 or 8 consecutive tokens, so every memory
 // instruction of a wave moves 1 KB of one token row; the K-1 rows before a run
 // are read again by the next run (an L2 hit).  All loads of a run are issued
 // before its first store, so they are in flight together.  The four waves of
@@ -19,10 +19,7 @@
 
 namespace gdn {
 
-constexpr int CONV_RUN = 8;
-constexpr int CONV_TILE = 4 * CONV_RUN;  // tokens of a block
-
-template <typename TI, int K>
+template <typename TI, int K, int RUN>
 __global__ __launch_bounds__(256) void ssm_conv_kernel(SsmDims d, const int32_t *__restrict__ cu,
                                                        const TI *__restrict__ xbc,
                                                        const TI *__restrict__ w,
@@ -30,13 +27,13 @@ __global__ __launch_bounds__(256) void ssm_conv_kernel(SsmDims d, const int32_t 
                                                        const TI *hist, TI *hist_out,
                                                        TI *__restrict__ out)
 {
-    constexpr int V = Vec16<TI>::n;
+    constexpr int V = Vec16<TI>::n, TILE = 4 * RUN;  // TILE: tokens of a block
     typedef typename Vec16<TI>::type vec;
     SeqTile st;
-    if (!find_tile(cu, d.n_seq, d.T, CONV_TILE, blockIdx.x, st)) return;
+    if (!find_tile(cu, d.n_seq, d.T, TILE, blockIdx.x, st)) return;
     const int c0 = (blockIdx.y * 64 + (threadIdx.x & 63)) * V;
     const int len = st.end - st.begin;
-    const int t0 = st.c * CONV_TILE + (threadIdx.x >> 6) * CONV_RUN;
+    const int t0 = st.c * TILE + (threadIdx.x >> 6) * RUN;
     if (c0 >= d.C || (t0 >= len && t0 > 0)) return;
 
     const TI *row0 = xbc + st.begin * d.xbc_stride + c0;
@@ -47,21 +44,21 @@ __global__ __launch_bounds__(256) void ssm_conv_kernel(SsmDims d, const int32_t 
         return hist ? ld16(h0 + (int64_t)e * d.C) : vec(TI(0));
     };
 
-    vec wk[K], x[CONV_RUN + K - 1], b = vec(TI(0)), nh[K - 1];
+    vec wk[K], x[RUN + K - 1], b = vec(TI(0)), nh[K - 1];
 #pragma unroll
     for (int k = 0; k < K; ++k) wk[k] = ld16(w + (int64_t)c0 * K + k * V);
     if (bias) b = ld16(bias + c0);
 #pragma unroll
-    for (int i = 0; i < CONV_RUN + K - 1; ++i) x[i] = t0 + i < len + K - 1 ? load(t0 + i) : vec(TI(0));
+    for (int i = 0; i < RUN + K - 1; ++i) x[i] = t0 + i < len + K - 1 ? load(t0 + i) : vec(TI(0));
     const bool carry = t0 == 0 && hist_out;
     if (carry) {
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) nh[j] = load(len + j);
     }
 
-    vec o[CONV_RUN];
+    vec o[RUN];
 #pragma unroll
-    for (int i = 0; i < CONV_RUN; ++i) {
+    for (int i = 0; i < RUN; ++i) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float acc = (float)b[v];
@@ -75,7 +72,7 @@ __global__ __launch_bounds__(256) void ssm_conv_kernel(SsmDims d, const int32_t 
     }
     TI *o0 = out + (int64_t)(st.begin + t0) * d.C + c0;
 #pragma unroll
-    for (int i = 0; i < CONV_RUN; ++i)
+    for (int i = 0; i < RUN; ++i)
         if (t0 + i < len) st16(o0 + (int64_t)i * d.C, o[i]);
     if (carry) {
         TI *n0 = hist_out + (int64_t)st.n * (K - 1) * d.C + c0;
@@ -84,24 +81,36 @@ __global__ __launch_bounds__(256) void ssm_conv_kernel(SsmDims d, const int32_t 
     }
 }
 
-template <typename TI, int K>
+template <typename TI, int K, int RUN>
 static void launch_conv_t(const SsmDims &d, const SsmConvArgs &a, hipStream_t st)
 {
     constexpr int V = Vec16<TI>::n;
-    const dim3 grid((unsigned)(d.T / CONV_TILE + d.n_seq), (unsigned)((d.C / V + 63) / 64));
-    hipLaunchKernelGGL((ssm_conv_kernel<TI, K>), grid, dim3(256), 0, st, d, a.cu,
+    const dim3 grid((unsigned)(d.T / (4 * RUN) + d.n_seq), (unsigned)((d.C / V + 63) / 64));
+    hipLaunchKernelGGL((ssm_conv_kernel<TI, K, RUN>), grid, dim3(256), 0, st, d, a.cu,
                        static_cast<const TI *>(a.xbc), static_cast<const TI *>(a.conv_w),
                        static_cast<const TI *>(a.conv_b), static_cast<const TI *>(a.hist),
                        static_cast<TI *>(a.hist_out), static_cast<TI *>(a.out));
+}
+
+// Runs of 8 tokens read a run's K-1 leading rows again less often; runs of 4
+// make twice the waves, which a launch of less than 8 waves a SIMD (of 1024)
+// needs.  Measured: 37 tokens of 512 fp32 channels 5.1 us by 8, 3.9 by 4; 2048
+// of 4352 fp16 12.5 and 11.5; 27135 of 6144 bf16 148 (4.5 TB/s) and 152.
+template <typename TI, int K>
+static void launch_conv_k(const SsmDims &d, const SsmConvArgs &a, hipStream_t st)
+{
+    const int64_t waves = d.T * (d.C / Vec16<TI>::n) / (64 * 8);
+    if (waves < 8192) launch_conv_t<TI, K, 4>(d, a, st);
+    else launch_conv_t<TI, K, 8>(d, a, st);
 }
 
 hipError_t launch_ssm_conv(const gdn_ssm_shape &s, const SsmConvArgs &a, hipStream_t st)
 {
     const SsmDims d = ssm_dims(s);
     GDN_SSM_IO(s.io_dtype,
-        if (s.conv_width == 2) launch_conv_t<TI, 2>(d, a, st);
-        else if (s.conv_width == 3) launch_conv_t<TI, 3>(d, a, st);
-        else launch_conv_t<TI, 4>(d, a, st);)
+        if (s.conv_width == 2) launch_conv_k<TI, 2>(d, a, st);
+        else if (s.conv_width == 3) launch_conv_k<TI, 3>(d, a, st);
+        else launch_conv_k<TI, 4>(d, a, st);)
     return hipGetLastError();
 }
 

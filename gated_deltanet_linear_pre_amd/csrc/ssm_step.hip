@@ -118,16 +118,20 @@ __global__ __launch_bounds__(256) void ssm_hist_shift_kernel(SsmDims d, int K, c
     st16(h + (int64_t)(K - 2) * d.C, ld16(xbc + n * d.xbc_stride + c));
 }
 
+// 64 rows a block (R = 2) form a head's B and C half as often as 32 do; 32 make
+// more blocks, which a launch of less than 2048 (8 a CU) needs.  Measured, 64
+// heads of 64, N = 128: one sequence 4.6 us by 64, 4.2 by 32; 64 sequences 50.6
+// (5.4 TB/s) and 52.3.
 template <typename TI, typename TO, int N, int K>
 static void launch_step_t(const SsmDims &d, const SsmStepArgs &a, hipStream_t st)
 {
     const bool in_place = a.hist_out && a.hist_out == a.hist;
-    constexpr int R = 1;
-    const int tiles = (d.P + 32 * R - 1) / (32 * R);
+    const bool wide = (int64_t)d.n_seq * d.H * ((d.P + 31) / 32) >= 2048 && d.P > 32;
+    const int tiles = (d.P + (wide ? 63 : 31)) / (wide ? 64 : 32);
     const unsigned gy = d.n_seq < 32768 ? d.n_seq : 32768;
     const dim3 grid(d.H * tiles, gy, (d.n_seq + gy - 1) / gy);
-    hipLaunchKernelGGL((ssm_step_kernel<TI, TO, N, K, R>), grid, dim3(256), 0, st, d, tiles,
-                       static_cast<const TI *>(a.xbc), static_cast<const TI *>(a.conv_w),
+    hipLaunchKernelGGL((wide ? ssm_step_kernel<TI, TO, N, K, 2> : ssm_step_kernel<TI, TO, N, K, 1>), grid, dim3(256), 0, st, d,
+                       tiles, static_cast<const TI *>(a.xbc), static_cast<const TI *>(a.conv_w),
                        static_cast<const TI *>(a.conv_b), static_cast<const TI *>(a.dt), a.A_log,
                        a.dt_bias, a.D, static_cast<const TI *>(a.hist),
                        in_place ? nullptr : static_cast<TI *>(a.hist_out), a.state, a.state_out,
