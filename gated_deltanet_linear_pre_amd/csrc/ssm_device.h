@@ -94,14 +94,42 @@ __device__ __forceinline__ bool find_tile(const int32_t *__restrict__ cu, int n_
 }
 
 // ---- step size and log decay ----------------------------------------------
+// e^x for x <= 0 to about 2 ulp at any size: the rounding of x log2(e), which
+// the hardware's 2^p does not see, is put back to first order
+__device__ __forceinline__ float exp_neg(float x)
+{
+    const float p = x * 1.44269502f;
+    float r = __builtin_fmaf(x, 1.44269502f, -p);
+    r = __builtin_fmaf(x, 1.92596299e-8f, r);  // log2(e) beyond its first float
+    return __builtin_amdgcn_exp2f(p) * __builtin_fmaf(r, 0.693147181f, 1.0f);
+}
+
+// log(1 + e) for 0 <= e <= 1 to about 3 ulp: 2 atanh(s), s = e / (2 + e) <= 1/3,
+// by its series; s^17 / 17 is below 2^-30 of the sum
+__device__ __forceinline__ float log1p_unit(float e)
+{
+    const float d = 2.0f + e, q = __builtin_amdgcn_rcpf(d);
+    float s = e * q;
+    s = __builtin_fmaf(__builtin_fmaf(-s, d, e), q, s);
+    const float t = s * s;
+    float v = 1.0f / 15.0f;
+    v = __builtin_fmaf(v, t, 1.0f / 13.0f);
+    v = __builtin_fmaf(v, t, 1.0f / 11.0f);
+    v = __builtin_fmaf(v, t, 1.0f / 9.0f);
+    v = __builtin_fmaf(v, t, 1.0f / 7.0f);
+    v = __builtin_fmaf(v, t, 1.0f / 5.0f);
+    v = __builtin_fmaf(v, t, 1.0f / 3.0f);
+    return 2.0f * __builtin_fmaf(s * t, v, s);
+}
+
 // dt = clamp(softplus(raw + bias)), lam = -exp(A_log) dt.  A NaN stays one (the
 // comparisons fail).  lam is bounded at -200, e^-200 being 0 in fp32, so that
 // sums of log decays stay finite and their differences exact.
 __device__ __forceinline__ void step_size(float raw, float bias, float neg_a, float dt_min,
                                           float dt_max, float &dt, float &lam)
 {
-    const float u = raw + bias;
-    float v = (u > 0.f ? u : 0.f) + log1pf(expf(-fabsf(u)));
+    const float u = raw + bias, m = fabsf(u);
+    float v = (u > 0.f ? u : 0.f) + log1p_unit(exp_neg(m > 150.f ? -150.f : -m));
     v = u != u ? u : v;
     v = v < dt_min ? dt_min : v;
     v = v > dt_max ? dt_max : v;

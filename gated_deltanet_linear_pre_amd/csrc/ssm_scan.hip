@@ -51,7 +51,7 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 template <typename T> struct Mat;
 template <> struct Mat<bf16> {
     typedef bf16 frag __attribute__((ext_vector_type(8)));
-    static constexpr int Q = 64, STATE_PARTS = 3;
+    static constexpr int STATE_PARTS = 3;
     static constexpr bool scaled = false;
     static __device__ __forceinline__ f4 mma(frag a, frag b, f4 c)
     {
@@ -60,7 +60,7 @@ template <> struct Mat<bf16> {
 };
 template <> struct Mat<_Float16> {
     typedef _Float16 frag __attribute__((ext_vector_type(8)));
-    static constexpr int Q = 64, STATE_PARTS = 2;
+    static constexpr int STATE_PARTS = 2;
     static constexpr bool scaled = true;
     static __device__ __forceinline__ f4 mma(frag a, frag b, f4 c)
     {
@@ -70,7 +70,7 @@ template <> struct Mat<_Float16> {
 // fp32: eight 4-deep products; product i contracts value i of every lane group
 template <> struct Mat<float> {
     typedef float frag __attribute__((ext_vector_type(8)));
-    static constexpr int Q = 32, STATE_PARTS = 1;
+    static constexpr int STATE_PARTS = 1;
     static constexpr bool scaled = false;
     static __device__ __forceinline__ f4 mma(frag a, frag b, f4 c)
     {
@@ -79,6 +79,12 @@ template <> struct Mat<float> {
         return c;
     }
 };
+
+// Tokens of a chunk.  64 halve the times that S is split into operands; with
+// N = 256 or fp32 only 32 leave LDS for two blocks on a CU (N = 256, bf16, 2005
+// tokens of 32 heads of 128: 92 us by 32, 101 by 64; N = 128, 8192 tokens of
+// 64 heads of 64, fp16: 104 us by 32 with three blocks on a CU, 90 by 64 with two)
+template <typename T, int N> constexpr int chunk_tokens() { return sizeof(T) == 4 || N == 256 ? 32 : 64; }
 
 // v = sum of PARTS values of the matrix type, each the nearest to what the
 // ones before it leave.  Two values at a time: their conversion and packing
@@ -257,20 +263,19 @@ constexpr int BATCH = 256;  // tokens whose decays are formed at a time, one a t
 // Rows of C and X are 32 bytes longer, those of M (also written in 8-byte
 // columns) 16.  Measured in cycles of an instruction, 4 waves reading: 16-byte
 // row reads 4.1 at 32 bytes, 8.1 at 16; transposing reads 4.1; 8-byte ones 4.8.
-template <typename TI, int N, int PARTS, bool OUT> struct __attribute__((aligned(16))) ScanShared {
-    static constexpr int Q = Mat<TI>::Q, E16 = 16 / sizeof(TI), REFS = Q / 16 - 1;
+template <typename TI, int N, int PARTS> struct __attribute__((aligned(16))) ScanShared {
+    static constexpr int Q = chunk_tokens<TI, N>(), E16 = 16 / sizeof(TI), REFS = Q / 16 - 1;
     static constexpr int BP = N + 40 / sizeof(TI), CP = N + 2 * E16, XP = 64 + 2 * E16, MP = Q + E16;
-    TI C[OUT ? Q : 1][CP];
+    TI C[Q][CP];
     TI X[Q][XP];
-    TI M[OUT ? PARTS : 1][OUT ? Q : 1][MP];
+    TI M[PARTS][Q][MP];
     TI B[Q][BP];
-    float2 lam[OUT ? BATCH : 1];                       // L_t in two floats
-    float dt[OUT ? BATCH : 1], E[OUT ? BATCH : 1];     // dt_t, exp(L_t)
-    float W[BATCH];              // exp(L_end - L_t) dt_t, to the end of the chunk (without outputs: of the batch)
-    float F[OUT ? BATCH : 1];    // exp(L_t - L_r), r the first token of t's tile of 16
-    float G[REFS][OUT ? BATCH : 1];  // exp(L_r - L_t) dt_t, r the first token of a later tile
+    float2 lam[BATCH];           // L_t in two floats
+    float dt[BATCH], E[BATCH];   // dt_t, exp(L_t)
+    float W[BATCH];              // exp(L_Q - L_t) dt_t
+    float F[BATCH];              // exp(L_t - L_r), r the first token of t's tile of 16
+    float G[REFS][BATCH];        // exp(L_r - L_t) dt_t, r the first token of a later tile
     float alpha[BATCH / Q];      // exp(L_Q)
-    double total[4];             // log decay of a wave's 64 tokens (without outputs)
     float mscale[Q];             // fp16: 1 / scale of M's row t
 };
 
@@ -285,42 +290,72 @@ struct ScanArgsT {
     int tile;          // tokens of a segment
 };
 
-// OUT: the outputs (and the end state of sequences of one segment); else the
-// segments' own end states and decays.  PARTS: parts of S and M.
-template <typename TI, typename TO, int N, int PARTS, bool OUT>
-__global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDims d, ScanArgsT a)
+// A block's part of the work: segment b.slot of a sequence, rows 64 b.pt.. of
+// the state of head b.h
+struct Part {
+    int64_t slot, row;       // row: the segment's first token row
+    int n, h, pt, n_tok;     // sequence, ..., tokens of the segment
+    int cols;                // rows of the state that are there, at most 64
+    int xc, bc, cc;          // first channels of x, B and C
+    bool single;             // the sequence is one segment
+};
+__device__ __forceinline__ bool locate(const SsmDims &d, const ScanArgsT &a, Part &b)
+{
+    SeqTile st;
+    b.slot = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
+    if (b.slot >= d.T / a.tile + d.n_seq) return false;
+    if (!find_tile(a.cu, d.n_seq, d.T, a.tile, (int)b.slot, st)) return false;
+    const int len = st.end - st.begin, first = st.c * a.tile, pt_n = (d.P + 63) / 64;
+    b.n = st.n;
+    b.single = len <= a.tile;
+    b.n_tok = len - first < a.tile ? len - first : a.tile;
+    b.row = st.begin + first;
+    // blocks go to the 8 XCDs in turn: neighbouring heads, which share B and C,
+    // go to one XCD and its L2
+    const int bx = gridDim.x % 8 ? blockIdx.x : blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
+    b.h = bx / pt_n;
+    b.pt = bx - b.h * pt_n;
+    b.cols = d.P - b.pt * 64 < 64 ? d.P - b.pt * 64 : 64;
+    const int grp = b.h / d.hg;
+    b.xc = b.h * d.P + b.pt * 64;
+    b.bc = d.H * d.P + grp * d.N;
+    b.cc = b.bc + d.G * d.N;
+    return true;
+}
+
+// 16 bytes at a uniform base and a 32-bit byte offset of the lane: one register
+// for the addresses of all rows a thread moves
+template <typename T>
+__device__ __forceinline__ typename Vec16<T>::type ld16_at(const T *base, uint32_t bytes)
+{
+    return ld16(reinterpret_cast<const T *>(reinterpret_cast<const char *>(base) + bytes));
+}
+
+// The outputs of every segment, and the end state of a sequence of one segment.
+// PARTS: parts of S and M.
+template <typename TI, typename TO, int N, int PARTS>
+__global__ __launch_bounds__(256, 2) void ssm_chunk_kernel(SsmDims d, ScanArgsT a)
 {
     typedef Mat<TI> MT;
     typedef typename MT::frag frag;
-    typedef ScanShared<TI, N, PARTS, OUT> Shared;
-    constexpr int Q = MT::Q, SP = MT::STATE_PARTS, J = N / 32, TT = Q / 16, KK = Q / 32;
+    typedef ScanShared<TI, N, PARTS> Shared;
+    constexpr int Q = chunk_tokens<TI, N>(), SP = MT::STATE_PARTS, J = N / 32, TT = Q / 16, KK = Q / 32;
     constexpr int V = Vec16<TI>::n;
     typedef typename Vec16<TI>::type vec;
     constexpr int NB = Q * N / V / 256;  // vectors of B (and C) a thread moves
     constexpr int NX = Q * 64 / V / 256;
-    constexpr bool DIRECT = !OUT && !MT::scaled && N <= 128;  // products accumulate onto S itself
     __shared__ Shared sh;
 
-    SeqTile st;
-    const int64_t slot = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
-    if (slot >= d.T / a.tile + d.n_seq) return;
-    if (!find_tile(a.cu, d.n_seq, d.T, a.tile, (int)slot, st)) return;
-    const int len = st.end - st.begin;
-    const bool single = len <= a.tile;
-    if (!OUT && single) return;
-    const int pt_n = (d.P + 63) / 64;
-    const int h = blockIdx.x / pt_n, pt = blockIdx.x - h * pt_n;
-    const int grp = h / d.hg;
+    Part b;
+    if (!locate(d, a, b)) return;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int p0 = pt * 64 + w * 16;      // of this wave
-    const bool mine = p0 < d.P;           // (a wave past P only helps with loads and M)
-    const int cols = d.P - pt * 64 < 64 ? d.P - pt * 64 : 64;
-    const int first = st.c * a.tile;      // in the sequence
-    const int n_tok = len - first < a.tile ? len - first : a.tile;
-    const TI *xrow = static_cast<const TI *>(a.xbc) + (int64_t)(st.begin + first) * d.C;
-    const TI *dtp = static_cast<const TI *>(a.dt) + (int64_t)(st.begin + first) * d.dt_stride + h;
-    const int xc = h * d.P + pt * 64, bc = d.H * d.P + grp * N, cc = bc + d.G * N;
+    const int p0 = b.pt * 64 + w * 16;  // of this wave
+    const bool mine = p0 < d.P;         // (a wave past P only helps with loads and M)
+    const bool single = b.single;
+    const int n_tok = b.n_tok, h = b.h;
+    const TI *xrow = static_cast<const TI *>(a.xbc) + b.row * d.C;
+    const TI *dtp = static_cast<const TI *>(a.dt) + b.row * d.dt_stride + h;
 
     // ---- state: lane (g, p = c), n = 32j + 8g + 4a + i.  fp16: S stands
     // for S * sdown, a power of two of row p that the last chunk's products needed.
@@ -328,48 +363,45 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
     float sdown = 1.f;
     const int64_t head_at = ((int64_t)h * d.P + p0 + c) * N + 8 * g;
     const int64_t seq_size = (int64_t)d.H * d.P * N;
-    const float neg_a = -expf(a.A_log[h]), dt_bias = a.dt_bias[h], Dh = OUT && a.D ? a.D[h] : 0.f;
-    double total = 0.0;       // log decay of the segment (without outputs)
-    float batch_alpha = 1.f;  // decay of a batch
+    const float neg_a = -expf(a.A_log[h]), dt_bias = a.dt_bias[h], Dh = a.D ? a.D[h] : 0.f;
 
     // ---- rows of a chunk in registers: vector i of a thread is row
     // i*RB + tid / (N/V) of B and C, i*RX + tid / (64/V) of X
     constexpr int RB = 256 * V / N, RX = 256 * V / 64;
-    vec rB[NB], rC[OUT ? NB : 1], rX[NX];
+    vec rB[NB], rC[NB], rX[NX];
     const int brow = tid / (N / V), bcol = tid % (N / V) * V, xr = tid / (64 / V), xcol = tid % (64 / V) * V;
     // (byte offsets of 32 bits beside a uniform base: one register for all rows)
     const uint32_t ob = ((uint32_t)brow * d.C + bcol) * sizeof(TI);
-    const uint32_t ox = ((uint32_t)xr * d.C + (xcol < cols ? xcol : 0)) * sizeof(TI);
+    const uint32_t ox = ((uint32_t)xr * d.C + (xcol < b.cols ? xcol : 0)) * sizeof(TI);
     const uint32_t oy = ((uint32_t)c * d.H * d.P + 4 * g) * sizeof(TO);
-    auto at = [](const TI *base, uint32_t bytes) { return ld16(reinterpret_cast<const TI *>(reinterpret_cast<const char *>(base) + bytes)); };
     auto fetch = [&](int t0) {
         const TI *base = xrow + (int64_t)t0 * d.C;
         if (t0 + Q <= n_tok) {
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
-                rB[i] = at(base + bc + (int64_t)i * RB * d.C, ob);
-                if (OUT) rC[i] = at(base + cc + (int64_t)i * RB * d.C, ob);
+                rB[i] = ld16_at(base + b.bc + (int64_t)i * RB * d.C, ob);
+                rC[i] = ld16_at(base + b.cc + (int64_t)i * RB * d.C, ob);
             }
 #pragma unroll
-            for (int i = 0; i < NX; ++i) rX[i] = at(base + xc + (int64_t)i * RX * d.C, ox);
+            for (int i = 0; i < NX; ++i) rX[i] = ld16_at(base + b.xc + (int64_t)i * RX * d.C, ox);
         } else {  // rows past the end are zero
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 const bool in = t0 + i * RB + brow < n_tok;
-                rB[i] = in ? at(base + bc + (int64_t)i * RB * d.C, ob) : vec(TI(0));
-                if (OUT) rC[i] = in ? at(base + cc + (int64_t)i * RB * d.C, ob) : vec(TI(0));
+                rB[i] = in ? ld16_at(base + b.bc + (int64_t)i * RB * d.C, ob) : vec(TI(0));
+                rC[i] = in ? ld16_at(base + b.cc + (int64_t)i * RB * d.C, ob) : vec(TI(0));
             }
 #pragma unroll
             for (int i = 0; i < NX; ++i)
-                rX[i] = t0 + i * RX + xr < n_tok ? at(base + xc + (int64_t)i * RX * d.C, ox) : vec(TI(0));
+                rX[i] = t0 + i * RX + xr < n_tok ? ld16_at(base + b.xc + (int64_t)i * RX * d.C, ox) : vec(TI(0));
         }
     };
     TI raw = tid < n_tok ? dtp[tid * d.dt_stride] : TI(0);
     fetch(0);
     const float *S0 = nullptr;
-    if (OUT && mine) {
-        if (!single) S0 = a.seg_state + slot * seq_size + head_at;
-        else if (a.state) S0 = a.state + st.n * seq_size + head_at;
+    if (mine) {
+        if (!single) S0 = a.seg_state + b.slot * seq_size + head_at;
+        else if (a.state) S0 = a.state + b.n * seq_size + head_at;
     }
 #pragma unroll
     for (int j = 0; j < J; ++j)
@@ -379,7 +411,7 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
 
     // M's t tile of a wave: the two blocks that usually share a CU take them
     // in opposite order (tile t costs t + 1 products)
-    const int mt = TT == 4 && (((int64_t)slot * gridDim.x + blockIdx.x) >> 8 & 1) ? 3 - w : w;
+    const int mt = TT == 4 && ((b.slot * gridDim.x + blockIdx.x) >> 8 & 1) ? 3 - w : w;
 
     // ---- M's rows t of tile T: D = B C^T has rows s, lane (g, t = c)
     auto form_m = [&](auto tile, int bt) {
@@ -445,7 +477,7 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
         }
         __builtin_amdgcn_sched_barrier(0);
     };
-    if (OUT) {  // the tiles of M above the diagonal that a 32-deep product touches
+    {  // the tiles of M above the diagonal that a 32-deep product touches
         typedef TI t4 __attribute__((ext_vector_type(4)));
         if (w < KK)
 #pragma unroll
@@ -462,37 +494,21 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
             const bool in = t0 + tid < n_tok;
             float dt = 0.f, lam = 0.f;
             if (in) step_size((float)raw, dt_bias, neg_a, d.dt_min, d.dt_max, dt, lam);
-            constexpr int QS = OUT ? Q : 64;  // (without outputs only the batch's end matters)
-            const double L = scan64<QS>(lam);
-            double LQ = lane64<QS>(L, QS - 1, lane);
-            if (OUT) {
-                const float hi = (float)L;
-                sh.lam[tid] = make_float2(hi, (float)(L - (double)hi));
-                sh.dt[tid] = dt;
-                sh.E[tid] = exp_fast(hi);
-                const int place = lane & (Q - 1);
-                double first_of_tile = lane64<Q>(L, 0, lane);
+            const double L = scan64<Q>(lam), LQ = lane64<Q>(L, Q - 1, lane);
+            const float hi = (float)L;
+            sh.lam[tid] = make_float2(hi, (float)(L - (double)hi));
+            sh.dt[tid] = dt;
+            sh.E[tid] = exp_fast(hi);
+            const int place = lane & (Q - 1);
+            double first_of_tile = lane64<Q>(L, 0, lane);
 #pragma unroll
-                for (int r = 1; r < TT; ++r) {
-                    const double Lr = lane64<Q>(L, 16 * r, lane);
-                    if (place >= 16 * r) first_of_tile = Lr;
-                    sh.G[r - 1][tid] = place < 16 * r ? exp_fast((float)(Lr - L)) * dt : 0.f;
-                }
-                sh.F[tid] = exp_fast((float)(L - first_of_tile));
-                if (place == 0) sh.alpha[tid / Q] = exp_fast((float)LQ);
-            } else {
-                if (lane == 0) sh.total[w] = LQ;
-                lds_sync();
-                double all = 0.0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const double o = sh.total[i];
-                    all += o;
-                    if (i > w) LQ += o;
-                }
-                batch_alpha = exp_fast((float)all);
-                total += all;
+            for (int r = 1; r < TT; ++r) {
+                const double Lr = lane64<Q>(L, 16 * r, lane);
+                if (place >= 16 * r) first_of_tile = Lr;
+                sh.G[r - 1][tid] = place < 16 * r ? exp_fast((float)(Lr - L)) * dt : 0.f;
             }
+            sh.F[tid] = exp_fast((float)(L - first_of_tile));
+            if (place == 0) sh.alpha[tid / Q] = exp_fast((float)LQ);
             sh.W[tid] = exp_fast((float)(LQ - L)) * dt;
             const int nt = t0 + BATCH + tid;
             raw = nt < n_tok ? dtp[nt * d.dt_stride] : TI(0);
@@ -500,25 +516,25 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             store_b(&sh.B[i * RB + brow][0], bcol, rB[i]);
-            if (OUT) st16(&sh.C[i * RB + brow][bcol], rC[i]);
+            st16(&sh.C[i * RB + brow][bcol], rC[i]);
         }
 #pragma unroll
         for (int i = 0; i < NX; ++i) st16(&sh.X[i * RX + xr][xcol], rX[i]);
         lds_sync();
-        if (!OUT) fetch(t0 + Q);
 
         const int rows = n_tok - t0 < Q ? n_tok - t0 : Q;  // (the others are zero)
         // Each product below loads all its operands from LDS, then issues its
         // matrix instructions, and its results are taken before the next
         // product's loads: no load is given registers of an operand in use.
         f4 acc[TT];
-        if (OUT) {
+        {
             if (mt == 0) form_m(std::integral_constant<int, 0>{}, bt);
             else if (mt == 1) form_m(std::integral_constant<int, 1>{}, bt);
             else if (TT > 2) {
                 if (mt == 2) form_m(std::integral_constant<int, (TT > 2 ? 2 : 0)>{}, bt);
                 else form_m(std::integral_constant<int, (TT > 2 ? 3 : 0)>{}, bt);
             }
+            __builtin_amdgcn_s_setprio(2);
             if (mine) {
                 // ---- y^T = S C^T: rows p, lane (g, t = c); then exp(L_t)
                 frag cf[J][TT];
@@ -564,15 +580,15 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        if (OUT) fetch(t0 + Q);  // (past the end: zeros; without a branch, as the old values would live on beside it)
+        fetch(t0 + Q);  // (past the end: zeros; without a branch, as the old values would live on beside it)
         frag xf[KK];
         if (mine) {
 #pragma unroll
             for (int k = 0; k < KK; ++k) xf[k] = col8(&sh.X[0][0], Shared::XP, 32 * k, 16 * w, lane);
             // ---- S <- alpha S + B^T (W x)
-            if (!OUT || t0 + Q < n_tok || (single && a.state_out)) {
+            if (t0 + Q < n_tok || (single && a.state_out)) {
                 float wt[KK][8];
-                float alpha = OUT ? sh.alpha[bt / Q] : bt ? 1.f : batch_alpha;
+                float alpha = sh.alpha[bt / Q];
 #pragma unroll
                 for (int k = 0; k < KK; ++k)
 #pragma unroll
@@ -596,12 +612,6 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
 #pragma unroll
                         for (int i = 0; i < 8; ++i) u[k][i] *= up;
                 }
-                if (DIRECT && bt == 0) {
-#pragma unroll
-                    for (int j = 0; j < J; ++j)
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) S[j][q] *= alpha;
-                }
                 frag uf[KK][SP];
 #pragma unroll
                 for (int k = 0; k < KK; ++k) split8<TI, SP>(u[k], uf[k]);
@@ -609,7 +619,7 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
                 // (in two parts of n, which bounds the registers: at N = 128 all
                 // of B^T at once spilled some, and 430 us on the packed batch
                 // of 27135 tokens became 490)
-                constexpr int JS = DIRECT || J < 2 ? J : J / 2;
+                constexpr int JS = J < 2 ? J : J / 2;
 #pragma unroll
                 for (int j0 = 0; j0 < J; j0 += JS) {
                     frag bf[JS][2][KK];
@@ -622,12 +632,6 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
                                 bf[j][q][k] = col8(&sh.B[0][0], Shared::BP, 32 * k, 32 * (j0 + j) + 16 * q, lane);
                     __builtin_amdgcn_sched_barrier(0);
                     f4 z[JS][2];
-                    if (DIRECT) {
-#pragma unroll
-                        for (int j = 0; j < JS; ++j)
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) z[j][q] = S[j0 + j][q];
-                    }
 #pragma unroll
                     for (int k = 0; k < KK; ++k)
 #pragma unroll
@@ -635,16 +639,17 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
 #pragma unroll
                             for (int j = 0; j < JS; ++j)
 #pragma unroll
-                                for (int q = 0; q < 2; ++q) z[j][q] = MT::mma(bf[j][q][k], uf[k][p], k + p || DIRECT ? z[j][q] : f4(0.f));
+                                for (int q = 0; q < 2; ++q) z[j][q] = MT::mma(bf[j][q][k], uf[k][p], k + p ? z[j][q] : f4(0.f));
 #pragma unroll
                     for (int j = 0; j < JS; ++j)
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) S[j0 + j][q] = DIRECT ? z[j][q] : S[j0 + j][q] * alpha + z[j][q];
+                        for (int q = 0; q < 2; ++q) S[j0 + j][q] = S[j0 + j][q] * alpha + z[j][q];
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
-        if (OUT) {
+        {
+            __builtin_amdgcn_s_setprio(0);
             lds_sync();  // M is complete
             if (mine) {
                 // ---- y^T += x^T M^T, and out
@@ -670,7 +675,7 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
                     for (int p = 0; p < PARTS; ++p)
 #pragma unroll
                         for (int t = 2 * k; t < TT; ++t) z[t] = MT::mma(xf[k], mf[p][t][k], z[t]);
-                char *yp = reinterpret_cast<char *>(static_cast<TO *>(a.y) + ((int64_t)(st.begin + first + t0) * d.H + h) * d.P + p0);
+                char *yp = reinterpret_cast<char *>(static_cast<TO *>(a.y) + ((b.row + t0) * d.H + h) * d.P + p0);
                 typedef TO o4 __attribute__((ext_vector_type(4)));
                 o4 o[TT];
 #pragma unroll
@@ -693,15 +698,202 @@ __global__ __launch_bounds__(256, N == 256 ? 1 : 2) void ssm_chunk_kernel(SsmDim
     __asm__ volatile("" : "+v"(lane_end));  // (the state's address is formed again, not kept)
     const int64_t end_at = ((int64_t)h * d.P + p0 + (lane_end & 15)) * N + 8 * (lane_end >> 4);
     float *to = nullptr;
-    if (!OUT) to = a.seg_state + slot * seq_size + end_at;
-    else if (single && a.state_out) to = a.state_out + st.n * seq_size + end_at;
+    if (single && a.state_out) to = a.state_out + b.n * seq_size + end_at;
     if (to) {
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
             for (int q = 0; q < 2; ++q) *reinterpret_cast<f4 *>(to + 32 * j + 4 * q) = MT::scaled ? S[j][q] * sdown : S[j][q];
     }
-    if (!OUT && tid == 0 && pt == 0) a.seg_decay[slot * d.H + h] = expf((float)total);
+}
+
+// ---- the end states of segments -------------------------------------------
+// S_end = sum_t exp(L_end - L_t) dt_t x_t B_t^T over a segment, from a zero state:
+// one long product with no step that waits for another, so its chunks may come
+// in any order.  They come from the last to the first, and a block stops where
+// the decay to the segment's end has fallen below e^-110: every weight before
+// that is 0 in fp32, and so is the segment's own decay.  (At the decays models
+// start from, half the heads' segments of 3584 tokens end within a few hundred.)
+template <typename TI, int N> struct __attribute__((aligned(16))) EndShared {
+    typedef ScanShared<TI, N, 1> S;
+    TI X[S::Q][S::XP];
+    TI B[S::Q][S::BP];
+    float W[BATCH];   // exp(L_end - L_t) dt_t
+    double total[4];  // log decay of 64 tokens
+};
+
+template <typename TI, int N>
+__global__ __launch_bounds__(256, 2) void ssm_end_kernel(SsmDims d, ScanArgsT a)
+{
+    typedef Mat<TI> MT;
+    typedef typename MT::frag frag;
+    typedef EndShared<TI, N> Shared;
+    constexpr int Q = chunk_tokens<TI, N>(), SP = MT::STATE_PARTS, J = N / 32, KK = Q / 32;
+    constexpr int V = Vec16<TI>::n, NB = Q * N / V / 256, NX = Q * 64 / V / 256;
+    constexpr int RB = 256 * V / N, RX = 256 * V / 64;
+    // products accumulate onto S itself, all of B^T's operands at once (fp16
+    // changes S's scale between chunks; N = 256 has no registers for it)
+    constexpr bool DIRECT = !MT::scaled && N <= 128;
+    constexpr int JS = DIRECT || J < 2 ? J : J / 2;
+    typedef typename Vec16<TI>::type vec;
+    __shared__ Shared sh;
+
+    Part b;
+    if (!locate(d, a, b) || b.single) return;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int p0 = b.pt * 64 + w * 16;
+    const bool mine = p0 < d.P;
+    const int n_tok = b.n_tok;
+    const TI *xrow = static_cast<const TI *>(a.xbc) + b.row * d.C;
+    const TI *dtp = static_cast<const TI *>(a.dt) + b.row * d.dt_stride + b.h;
+
+    int t0 = (n_tok - 1) / Q * Q;
+    const int first_raw = (t0 & ~(BATCH - 1)) + tid;
+    TI raw = first_raw < n_tok ? dtp[first_raw * d.dt_stride] : TI(0);
+    vec rB[NB], rX[NX];
+    const int brow = tid / (N / V), bcol = tid % (N / V) * V, xr = tid / (64 / V), xcol = tid % (64 / V) * V;
+    const uint32_t ob = ((uint32_t)brow * d.C + bcol) * sizeof(TI);
+    const uint32_t ox = ((uint32_t)xr * d.C + (xcol < b.cols ? xcol : 0)) * sizeof(TI);
+    auto fetch = [&](int t) {
+        const TI *base = xrow + (int64_t)t * d.C;
+        if (t + Q <= n_tok) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i) rB[i] = ld16_at(base + b.bc + (int64_t)i * RB * d.C, ob);
+#pragma unroll
+            for (int i = 0; i < NX; ++i) rX[i] = ld16_at(base + b.xc + (int64_t)i * RX * d.C, ox);
+        } else {  // rows past the end are zero
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+                rB[i] = t + i * RB + brow < n_tok ? ld16_at(base + b.bc + (int64_t)i * RB * d.C, ob) : vec(TI(0));
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+                rX[i] = t + i * RX + xr < n_tok ? ld16_at(base + b.xc + (int64_t)i * RX * d.C, ox) : vec(TI(0));
+        }
+    };
+    fetch(t0);
+
+    f4 S[J][2];
+#pragma unroll
+    for (int j = 0; j < J; ++j) S[j][0] = S[j][1] = f4(0.f);
+    float sdown = 1.f;
+    const float neg_a = -expf(a.A_log[b.h]), dt_bias = a.dt_bias[b.h];
+    double after = 0.0, all = 0.0;  // log decay after this batch, and of it
+    float rest[4];                  // log decay after each 64 tokens of it
+    bool fresh = true, faded = false;
+
+    for (; t0 >= 0; t0 -= Q) {
+        if (!fresh) lds_sync();  // every wave is done with the last chunk
+        const int bt = t0 & (BATCH - 1);
+        if (fresh || bt == BATCH - Q) {
+            after += all;
+            float dt = 0.f, lam = 0.f;
+            const int t = t0 - bt + tid;
+            if (t < n_tok) step_size((float)raw, dt_bias, neg_a, d.dt_min, d.dt_max, dt, lam);
+            const double L = scan64<64>(lam);
+            if (lane == 63) sh.total[w] = L;
+            lds_sync();
+            all = 0.0;
+            double to_end = after;  // after this wave's tokens
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+                rest[i] = (float)(after + all);
+                if (i == w) to_end = after + all;
+                all += sh.total[i];
+            }
+            sh.W[tid] = exp_fast((float)(lane64<64>(L, 63, lane) - L + to_end)) * dt;
+            const int nt = t - BATCH;
+            raw = nt >= 0 ? dtp[nt * d.dt_stride] : TI(0);
+        }
+        fresh = false;
+        const int quarter = bt / 64;
+        const float left = quarter == 0 ? rest[0] : quarter == 1 ? rest[1] : quarter == 2 ? rest[2] : rest[3];
+        faded = left < -110.f;
+        if (faded) break;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) store_b(&sh.B[i * RB + brow][0], bcol, rB[i]);
+#pragma unroll
+        for (int i = 0; i < NX; ++i) st16(&sh.X[i * RX + xr][xcol], rX[i]);
+        lds_sync();
+        fetch(t0 >= Q ? t0 - Q : 0);  // (without a branch, see the chunk kernel)
+
+        __builtin_amdgcn_s_setprio(2);
+        if (mine) {
+            frag xf[KK], bf[JS][2][KK];
+            float u[KK][8];
+            auto load_b = [&](int j0) {
+#pragma unroll
+                for (int j = 0; j < JS; ++j)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int k = 0; k < KK; ++k)
+                            bf[j][q][k] = col8(&sh.B[0][0], Shared::S::BP, 32 * k, 32 * (j0 + j) + 16 * q, lane);
+            };
+#pragma unroll
+            for (int k = 0; k < KK; ++k) {
+                xf[k] = col8(&sh.X[0][0], Shared::S::XP, 32 * k, 16 * w, lane);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[k][i] = sh.W[bt + 32 * k + 8 * g + i];
+            }
+            load_b(0);
+#pragma unroll
+            for (int k = 0; k < KK; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[k][i] *= (float)xf[k][i];
+            float scale = 1.f;  // of S before this chunk
+            if (MT::scaled) {
+                float most = 0.f, up;
+#pragma unroll
+                for (int k = 0; k < KK; ++k)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(u[k][i]));
+                scale = sdown;
+                scale_of(max_of_groups(most), up, sdown);
+                scale *= up;
+#pragma unroll
+                for (int k = 0; k < KK; ++k)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[k][i] *= up;
+            }
+            frag uf[KK][SP];
+#pragma unroll
+            for (int k = 0; k < KK; ++k) split8<TI, SP>(u[k], uf[k]);
+#pragma unroll
+            for (int j0 = 0; j0 < J; j0 += JS) {
+                if (j0) load_b(j0);
+                __builtin_amdgcn_sched_barrier(0);
+                f4 z[JS][2];
+#pragma unroll
+                for (int j = 0; j < JS; ++j)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) z[j][q] = DIRECT ? S[j0 + j][q] : f4(0.f);
+#pragma unroll
+                for (int k = 0; k < KK; ++k)
+#pragma unroll
+                    for (int p = 0; p < SP; ++p)
+#pragma unroll
+                        for (int j = 0; j < JS; ++j)
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) z[j][q] = MT::mma(bf[j][q][k], uf[k][p], z[j][q]);
+#pragma unroll
+                for (int j = 0; j < JS; ++j)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        S[j0 + j][q] = DIRECT ? z[j][q] : MT::scaled ? S[j0 + j][q] * scale + z[j][q] : S[j0 + j][q] + z[j][q];
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        __builtin_amdgcn_s_setprio(0);
+    }
+
+    if (tid == 0 && b.pt == 0) a.seg_decay[b.slot * d.H + b.h] = faded ? 0.f : expf((float)(after + all));
+    if (!mine) return;
+    float *to = a.seg_state + b.slot * ((int64_t)d.H * d.P * N) + ((int64_t)b.h * d.P + p0 + c) * N + 8 * g;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) *reinterpret_cast<f4 *>(to + 32 * j + 4 * q) = MT::scaled ? S[j][q] * sdown : S[j][q];
 }
 
 // Over the segments of a sequence: the state each starts from replaces its own
@@ -742,14 +934,12 @@ __global__ __launch_bounds__(256) void ssm_segment_kernel(SsmDims d, ScanArgsT a
 }
 
 // Tokens of a segment, in whole batches of decays: as many as make the launch
-// about as many blocks as the chip's 256 CUs hold at once, two a CU, or one
-// with N = 256, whose LDS and registers leave room for one.  Measured: 2048
-// tokens of 64 heads, N = 128, bf16: 256 blocks 50 us, 512 45, 1024 44;
-// 27135 packed tokens: 530, 398, 420; N = 256, 2005 tokens of 32 heads of 128:
-// 256 blocks 100 us, 512 119.
+// about as many blocks as the chip's 256 CUs hold at once, two a CU.  Measured:
+// 2048 tokens of 64 heads, N = 128, bf16: 256 blocks 50 us, 512 45, 1024 44;
+// 27135 packed tokens: 530, 398, 420.
 int segment_tokens(const SsmDims &d)
 {
-    const int64_t blocks = (int64_t)d.H * ((d.P + 63) / 64), room = d.N == 256 ? 256 : 512;
+    const int64_t blocks = (int64_t)d.H * ((d.P + 63) / 64), room = 512;
     int64_t tile = (d.T * blocks + room - 1) / room;
     tile = (tile + BATCH - 1) / BATCH * BATCH;
     return (int)(tile < BATCH ? BATCH : tile);
@@ -782,10 +972,10 @@ static void launch_scan_t(const SsmDims &d, const SsmScanArgs &a, bool segments,
     if (segments) {
         t.seg_state = static_cast<float *>(a.ws);
         t.seg_decay = reinterpret_cast<float *>(static_cast<char *>(a.ws) + round256((size_t)slots * d.H * d.P * N * sizeof(float)));
-        hipLaunchKernelGGL((ssm_chunk_kernel<TI, TI, N, 1, false>), grid((int64_t)d.H * pt_n, slots), dim3(256), 0, st, d, t);
+        hipLaunchKernelGGL((ssm_end_kernel<TI, N>), grid((int64_t)d.H * pt_n, slots), dim3(256), 0, st, d, t);
         hipLaunchKernelGGL(ssm_segment_kernel, grid(((int64_t)d.H * d.P * N / 4 + 255) / 256, d.n_seq), dim3(256), 0, st, d, t);
     }
-    hipLaunchKernelGGL((ssm_chunk_kernel<TI, TO, N, PARTS, true>), grid((int64_t)d.H * pt_n, slots), dim3(256), 0, st, d, t);
+    hipLaunchKernelGGL((ssm_chunk_kernel<TI, TO, N, PARTS>), grid((int64_t)d.H * pt_n, slots), dim3(256), 0, st, d, t);
 }
 
 template <typename TI, typename TO>
