@@ -80,11 +80,15 @@ template <> struct Mat<float> {
     }
 };
 
-// Tokens of a chunk.  64 halve the times that S is split into operands; with
-// N = 256 or fp32 only 32 leave LDS for two blocks on a CU (N = 256, bf16, 2005
-// tokens of 32 heads of 128: 92 us by 32, 101 by 64; N = 128, 8192 tokens of
-// 64 heads of 64, fp16: 104 us by 32 with three blocks on a CU, 90 by 64 with two)
-template <typename T, int N> constexpr int chunk_tokens() { return sizeof(T) == 4 || N == 256 ? 32 : 64; }
+// Tokens of a chunk.  64 halve the times that S is split into operands; 32 leave
+// LDS for two blocks on a CU with N = 256 or fp32, and for three with three
+// parts of S and M.  Measured: N = 256, bf16 to fp32, 2005 tokens of 32 heads of
+// 128: 92 us by 32, 101 by 64; N = 128, 2048 tokens of 64 heads of 64, bf16 to
+// fp32: 50 and 58; fp16 to fp16, 8192 tokens: 104 and 90.
+template <typename T, int N, int PARTS> constexpr int chunk_tokens()
+{
+    return sizeof(T) == 4 || N == 256 || (N == 128 && PARTS == 3) ? 32 : 64;
+}
 
 // v = sum of PARTS values of the matrix type, each the nearest to what the
 // ones before it leave.  Two values at a time: their conversion and packing
@@ -264,7 +268,7 @@ constexpr int BATCH = 256;  // tokens whose decays are formed at a time, one a t
 // columns) 16.  Measured in cycles of an instruction, 4 waves reading: 16-byte
 // row reads 4.1 at 32 bytes, 8.1 at 16; transposing reads 4.1; 8-byte ones 4.8.
 template <typename TI, int N, int PARTS> struct __attribute__((aligned(16))) ScanShared {
-    static constexpr int Q = chunk_tokens<TI, N>(), E16 = 16 / sizeof(TI), REFS = Q / 16 - 1;
+    static constexpr int Q = chunk_tokens<TI, N, PARTS>(), E16 = 16 / sizeof(TI), REFS = Q / 16 - 1;
     static constexpr int BP = N + 40 / sizeof(TI), CP = N + 2 * E16, XP = 64 + 2 * E16, MP = Q + E16;
     TI C[Q][CP];
     TI X[Q][XP];
@@ -334,12 +338,12 @@ __device__ __forceinline__ typename Vec16<T>::type ld16_at(const T *base, uint32
 // The outputs of every segment, and the end state of a sequence of one segment.
 // PARTS: parts of S and M.
 template <typename TI, typename TO, int N, int PARTS>
-__global__ __launch_bounds__(256, 2) void ssm_chunk_kernel(SsmDims d, ScanArgsT a)
+__global__ __launch_bounds__(256, N == 128 && PARTS == 3 ? 3 : 2) void ssm_chunk_kernel(SsmDims d, ScanArgsT a)
 {
     typedef Mat<TI> MT;
     typedef typename MT::frag frag;
     typedef ScanShared<TI, N, PARTS> Shared;
-    constexpr int Q = chunk_tokens<TI, N>(), SP = MT::STATE_PARTS, J = N / 32, TT = Q / 16, KK = Q / 32;
+    constexpr int Q = chunk_tokens<TI, N, PARTS>(), SP = MT::STATE_PARTS, J = N / 32, TT = Q / 16, KK = Q / 32;
     constexpr int V = Vec16<TI>::n;
     typedef typename Vec16<TI>::type vec;
     constexpr int NB = Q * N / V / 256;  // vectors of B (and C) a thread moves
@@ -728,7 +732,7 @@ __global__ __launch_bounds__(256, 2) void ssm_end_kernel(SsmDims d, ScanArgsT a)
     typedef Mat<TI> MT;
     typedef typename MT::frag frag;
     typedef EndShared<TI, N> Shared;
-    constexpr int Q = chunk_tokens<TI, N>(), SP = MT::STATE_PARTS, J = N / 32, KK = Q / 32;
+    constexpr int Q = chunk_tokens<TI, N, 1>(), SP = MT::STATE_PARTS, J = N / 32, KK = Q / 32;
     constexpr int V = Vec16<TI>::n, NB = Q * N / V / 256, NX = Q * 64 / V / 256;
     constexpr int RB = 256 * V / N, RX = 256 * V / 64;
     // products accumulate onto S itself, all of B^T's operands at once (fp16
