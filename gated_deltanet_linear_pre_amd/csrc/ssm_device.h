@@ -88,6 +88,7 @@ __device__ __forceinline__ bool find_tile(const int32_t *__restrict__ cu, int n_
     out.n = lo;
     out.begin = seq_bound(cu, lo, T);
     out.end = seq_bound(cu, lo + 1, T);
+    if (out.end < out.begin) out.end = out.begin;
     out.c = slot - (out.begin / tile + lo);
     if (out.c < 0) return false;  // (cu does not start at 0)
     return out.c == 0 || (int64_t)out.c * tile < (int64_t)out.end - out.begin;

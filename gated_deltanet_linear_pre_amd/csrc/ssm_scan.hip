@@ -967,6 +967,7 @@ static void launch_scan_t(const SsmDims &d, const SsmScanArgs &a, bool segments,
 {
     constexpr int PARTS = sizeof(TI) == 4 ? 1 : Mat<TI>::scaled ? 2 : sizeof(TO) == 4 ? 3 : 2;
     ScanArgsT t{a.cu, a.xbc, a.dt, a.A_log, a.dt_bias, a.D, a.state, a.state_out, a.y, nullptr, nullptr, segment_tokens(d)};
+    if (!segments) t.tile = 1 << 30;  // every sequence is one segment, whatever cu_seqlens holds
     const int64_t slots = d.T / t.tile + d.n_seq;
     const int pt_n = (d.P + 63) / 64;
     auto grid = [](int64_t x, int64_t yz) {

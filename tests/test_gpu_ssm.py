@@ -254,6 +254,87 @@ def test_scan_of_an_empty_batch_copies_the_state(gpu):
     assert torch.equal(S, L.state) and torch.equal(h, L.hist)
 
 
+def test_many_sequences(gpu):
+    # more sequences than a launch grid's second dimension takes in one piece
+    n = 40000
+    L = Layer([1] * n, H=1, P=16, G=1, N=32, K=2, io="f16")
+    banner("gdn_ssm_conv, scan, step: 40000 sequences")
+    out, hist = torch.empty(n, L.C, dtype=torch.float16, device="cuda"), torch.empty_like(L.hist)
+    ssm.gdn_ssm_conv(L.shape(), L.cu_t, L.raw, L.conv_w, L.conv_b, L.hist, hist, out)
+    y, S = L.run_scan("f32")
+    sy, sS, sh = torch.empty(n, 1, 16, device="cuda"), torch.empty_like(L.state), torch.empty_like(hist)
+    ssm.gdn_ssm_step(L.shape("f32"), L.raw, L.conv_w, L.conv_b, L.dt, L.A_log, L.dt_bias, L.D, L.hist, sh, L.state, sS, sy)
+    torch.cuda.synchronize()
+    assert torch.equal(sh, hist)
+    at = np.r_[0:3, 32766:32771, n - 3:n]  # around the grid's seam, and the ends
+    part = Layer([1] * len(at), H=1, P=16, G=1, N=32, K=2, io="f16")
+    pick = torch.from_numpy(at).cuda()
+    for k in ("proj", "xbc", "hist", "state"):
+        setattr(part, k, getattr(L, k)[pick].contiguous())
+    part.raw, part.dt = part.proj[:, :L.C], part.proj[:, L.C:L.C + 1]
+    for k in ("conv_w", "conv_b", "A_log", "dt_bias", "D"):
+        setattr(part, k, getattr(L, k))
+    part.check_scan(y[pick], S[pick], "f32")
+    c, ce, new = orc.conv(part.cu, f64(part.raw), f64(L.conv_w), f64(L.conv_b), f64(part.hist))
+    check("out", out[pick], c, orc.rounded(c, ce, "f16"))
+    assert np.array_equal(f64(hist[pick]), new)
+    dt, lam = part.steps()
+    ry, ey, rS, eS = orc.scan(part.cu, c, dt, lam, f64(L.D), f64(part.state), 1, 16, 1, 32, xbc_err=ce)
+    check("step y", sy[pick], ry, orc.rounded(ry, ey, "f32"))
+    check("step state", sS[pick], rS, orc.rounded(rS, eS, "f32"))
+
+
+def test_rows_past_32_bits(gpu):
+    # the last sequence lies behind 2^31 elements of xbc and y: the same bits as
+    # a call on its rows alone
+    H, P, G, N, tail = 64, 64, 1, 128, 70
+    C = H * P + 2 * G * N
+    T = (1 << 31) // (H * P) + 200
+    small = Layer([tail], H=H, P=P, G=G, N=N)
+    xbc = torch.zeros(T, C, dtype=torch.bfloat16, device="cuda")
+    dt = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    xbc[-tail:], dt[-tail:] = small.xbc, small.dt
+    y = torch.empty(T, H * P, dtype=torch.bfloat16, device="cuda")
+    state = torch.cat([torch.zeros_like(small.state), small.state])
+    S = torch.empty_like(state)
+    cu = torch.tensor([0, T - tail, T], dtype=torch.int32, device="cuda")
+    s = ssm.make_ssm_shape(H, P, G, N, 2, T, T - tail)
+    ws = torch.empty(ssm.gdn_ssm_scan_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    banner("gdn_ssm_scan, conv past 2^31 elements", T)
+    ssm.gdn_ssm_scan(s, cu, xbc, dt, small.A_log, small.dt_bias, small.D, state, S, y, ws)
+    ys, Ss = small.run_scan()
+    assert torch.equal(y[-tail:].view(tail, H, P), ys) and torch.equal(S[1:], Ss)
+    assert not y[:1000].any() and not y[T // 2:T // 2 + 1000].any() and not S[0].any()
+    # the conv of the same rows, its output over y's old place
+    hist = torch.zeros(2, 3, C, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(xbc)
+    ssm.gdn_ssm_conv(s, cu, xbc, small.conv_w, None, hist, hist, out)
+    one = torch.empty(tail, C, dtype=torch.bfloat16, device="cuda")
+    ssm.gdn_ssm_conv(small.shape(strided=False), small.cu_t, small.xbc, small.conv_w, None, None, None, one)
+    assert torch.equal(out[-tail:], one) and torch.equal(hist[1], small.xbc[-3:]) and not out[:1000].any()
+
+
+def test_bounds_outside_the_rows_are_taken_as_their_ends(gpu):
+    # cu_seqlens below 0, past total_T, and falling: no access leaves the
+    # buffers, and a call whose max_T is too small is right all the same
+    L = Layer([30, 90], H=2, P=64, G=1, N=64, io="bf16")
+    y, S = Guard((L.T, 2, 64), torch.bfloat16), Guard(tuple(L.state.shape), torch.float32)
+    out, hist = Guard((L.T, L.C), torch.bfloat16), Guard(tuple(L.hist.shape), torch.bfloat16)
+    for cu in ([-7, 30, 1 << 30], [40, 10, 120], [0, 120, 60]):
+        L.cu_t = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        banner("cu_seqlens", cu)
+        L.run_scan(state_out=S.t, y=y.t)
+        ssm.gdn_ssm_conv(L.shape(), L.cu_t, L.raw, L.conv_w, None, L.hist, hist.t, out.t)
+        torch.cuda.synchronize()
+        assert y.intact() and S.intact() and out.intact() and hist.intact()
+        if cu[1] == 30:
+            L.check_scan(y.t, S.t)
+    L = Layer([700], H=2, P=64, G=1, N=64, io="bf16")
+    banner("max_T too small")
+    y, S = L.run_scan(shape_kw=dict(max_T=1))
+    L.check_scan(y, S)
+
+
 # ----------------------------------------------------------------- the step
 @pytest.mark.parametrize("io,out", [("f32", "f32"), ("f16", "f16"), ("bf16", "bf16"), ("bf16", "f32")])
 @pytest.mark.parametrize("n,H,P,G,N,K", [
