@@ -27,11 +27,6 @@ __device__ __forceinline__ void st16(T *p, typename Vec16<T>::type v)
 {
     *reinterpret_cast<typename Vec16<T>::type *>(p) = v;
 }
-template <typename T>
-__device__ __forceinline__ void st16_nt(T *p, typename Vec16<T>::type v)
-{
-    __builtin_nontemporal_store(v, reinterpret_cast<typename Vec16<T>::type *>(p));
-}
 
 // 8 consecutive elements widened to fp32, and narrowed (to nearest even) back
 template <typename T>

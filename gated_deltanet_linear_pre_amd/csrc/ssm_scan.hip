@@ -13,9 +13,10 @@
 //
 // Segments.  A sequence's chunks follow one another, so a launch with few
 // (sequence, head) pairs cuts sequences into segments: a first kernel forms
-// every segment's own end state from zero and its decay, a small one runs over
-// the segments of a sequence and leaves the state each starts from, and the
-// third walks all segments at once for the outputs.
+// every segment's own end state from zero and its decay, and a last one walks
+// all segments at once for the outputs.  Between them a small kernel runs over
+// the segments of a sequence and leaves the state each starts from; where a
+// sequence has few, the last kernel's blocks do that as they start.
 //
 // gfx950 mapping.  A block of 4 waves takes one (segment, head, 64 state rows
 // p); wave w owns rows 16w..16w+15 of them, S in its accumulators as [n][p]
@@ -292,6 +293,8 @@ struct ScanArgsT {
     float *seg_state;  // [slot][H][P][N]
     float *seg_decay;  // [slot][H]
     int tile;          // tokens of a segment
+    bool joined;       // seg_state holds start states (else the segments' own end states)
+    bool copied;       // the last segment's place holds a copy of the sequence's state
 };
 
 // A block's part of the work: segment b.slot of a sequence, rows 64 b.pt.. of
@@ -299,9 +302,10 @@ struct ScanArgsT {
 struct Part {
     int64_t slot, row;       // row: the segment's first token row
     int n, h, pt, n_tok;     // sequence, ..., tokens of the segment
+    int c, after;            // segments of the sequence before it and after it
     int cols;                // rows of the state that are there, at most 64
     int xc, bc, cc;          // first channels of x, B and C
-    bool single;             // the sequence is one segment
+    bool single, last;       // the sequence is one segment; this is its last one
 };
 __device__ __forceinline__ bool locate(const SsmDims &d, const ScanArgsT &a, Part &b)
 {
@@ -311,8 +315,11 @@ __device__ __forceinline__ bool locate(const SsmDims &d, const ScanArgsT &a, Par
     if (!find_tile(a.cu, d.n_seq, d.T, a.tile, (int)b.slot, st)) return false;
     const int len = st.end - st.begin, first = st.c * a.tile, pt_n = (d.P + 63) / 64;
     b.n = st.n;
+    b.c = st.c;
+    b.after = len > first ? (len - first - 1) / a.tile : 0;
     b.single = len <= a.tile;
-    b.n_tok = len - first < a.tile ? len - first : a.tile;
+    b.last = len - first <= a.tile;
+    b.n_tok = b.last ? len - first : a.tile;
     b.row = st.begin + first;
     // blocks go to the 8 XCDs in turn: neighbouring heads, which share B and C,
     // go to one XCD and its L2
@@ -335,7 +342,7 @@ __device__ __forceinline__ typename Vec16<T>::type ld16_at(const T *base, uint32
     return ld16(reinterpret_cast<const T *>(reinterpret_cast<const char *>(base) + bytes));
 }
 
-// The outputs of every segment, and the end state of a sequence of one segment.
+// The outputs of every segment, and the end state of the last one of a sequence.
 // PARTS: parts of S and M.
 template <typename TI, typename TO, int N, int PARTS>
 __global__ __launch_bounds__(256, N == 128 && PARTS == 3 ? 3 : 2) void ssm_chunk_kernel(SsmDims d, ScanArgsT a)
@@ -356,7 +363,7 @@ __global__ __launch_bounds__(256, N == 128 && PARTS == 3 ? 3 : 2) void ssm_chunk
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int p0 = b.pt * 64 + w * 16;  // of this wave
     const bool mine = p0 < d.P;         // (a wave past P only helps with loads and M)
-    const bool single = b.single;
+    const bool keep = b.last && a.state_out;  // the end state is asked for
     const int n_tok = b.n_tok, h = b.h;
     const TI *xrow = static_cast<const TI *>(a.xbc) + b.row * d.C;
     const TI *dtp = static_cast<const TI *>(a.dt) + b.row * d.dt_stride + h;
@@ -404,7 +411,8 @@ __global__ __launch_bounds__(256, N == 128 && PARTS == 3 ? 3 : 2) void ssm_chunk
     fetch(0);
     const float *S0 = nullptr;
     if (mine) {
-        if (!single) S0 = a.seg_state + b.slot * seq_size + head_at;
+        if (!b.single && a.joined) S0 = a.seg_state + b.slot * seq_size + head_at;
+        else if (!b.single && a.copied) S0 = a.seg_state + (b.slot + b.after) * seq_size + head_at;
         else if (a.state) S0 = a.state + b.n * seq_size + head_at;
     }
 #pragma unroll
@@ -412,6 +420,34 @@ __global__ __launch_bounds__(256, N == 128 && PARTS == 3 ? 3 : 2) void ssm_chunk
 #pragma unroll
         for (int q = 0; q < 2; ++q)
             S[j][q] = S0 ? *reinterpret_cast<const f4 *>(S0 + 32 * j + 4 * q) : f4(0.f);
+    if (mine && !a.joined && b.c) {  // over the segments before this one
+        constexpr int JG = J < 4 ? J : 4, AHEAD = 3;  // loads in flight
+        const float *own0 = a.seg_state + (b.slot - b.c) * seq_size + head_at, *dec = a.seg_decay + (b.slot - b.c) * d.H + h;
+#pragma unroll
+        for (int j0 = 0; j0 < J; j0 += JG)
+            for (int s0 = 0; s0 < b.c; s0 += AHEAD) {
+                f4 own[AHEAD][JG][2];
+                float decay[AHEAD];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int s = s0 + i < b.c ? s0 + i : b.c - 1;
+                    decay[i] = dec[(int64_t)s * d.H];
+#pragma unroll
+                    for (int j = 0; j < JG; ++j)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            own[i][j][q] = *reinterpret_cast<const f4 *>(own0 + s * seq_size + 32 * (j0 + j) + 4 * q);
+                }
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i)
+                    if (s0 + i < b.c) {
+#pragma unroll
+                        for (int j = 0; j < JG; ++j)
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) S[j0 + j][q] = S[j0 + j][q] * decay[i] + own[i][j][q];
+                    }
+            }
+    }
 
     // M's t tile of a wave: the two blocks that usually share a CU take them
     // in opposite order (tile t costs t + 1 products)
@@ -590,7 +626,7 @@ __global__ __launch_bounds__(256, N == 128 && PARTS == 3 ? 3 : 2) void ssm_chunk
 #pragma unroll
             for (int k = 0; k < KK; ++k) xf[k] = col8(&sh.X[0][0], Shared::XP, 32 * k, 16 * w, lane);
             // ---- S <- alpha S + B^T (W x)
-            if (t0 + Q < n_tok || (single && a.state_out)) {
+            if (t0 + Q < n_tok || keep) {
                 float wt[KK][8];
                 float alpha = sh.alpha[bt / Q];
 #pragma unroll
@@ -701,9 +737,8 @@ __global__ __launch_bounds__(256, N == 128 && PARTS == 3 ? 3 : 2) void ssm_chunk
     int lane_end = threadIdx.x & 63;
     __asm__ volatile("" : "+v"(lane_end));  // (the state's address is formed again, not kept)
     const int64_t end_at = ((int64_t)h * d.P + p0 + (lane_end & 15)) * N + 8 * (lane_end >> 4);
-    float *to = nullptr;
-    if (single && a.state_out) to = a.state_out + b.n * seq_size + end_at;
-    if (to) {
+    if (keep) {
+        float *to = a.state_out + b.n * seq_size + end_at;
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -711,7 +746,7 @@ __global__ __launch_bounds__(256, N == 128 && PARTS == 3 ? 3 : 2) void ssm_chunk
     }
 }
 
-// ---- the end states of segments -------------------------------------------
+// ---- the end states of all segments of a sequence but its last -------------
 // S_end = sum_t exp(L_end - L_t) dt_t x_t B_t^T over a segment, from a zero state:
 // one long product with no step that waits for another, so its chunks may come
 // in any order.  They come from the last to the first, and a block stops where
@@ -748,6 +783,19 @@ __global__ __launch_bounds__(256, 2) void ssm_end_kernel(SsmDims d, ScanArgsT a)
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int p0 = b.pt * 64 + w * 16;
     const bool mine = p0 < d.P;
+    if (b.last) {
+        // the chunk kernel's block of this segment writes the sequence's state,
+        // perhaps before those of the other segments have read it: they read this copy
+        if (!a.copied || !mine) return;
+        const int64_t seq_size = (int64_t)d.H * d.P * N, at = ((int64_t)b.h * d.P + p0 + c) * N + 8 * g;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                *reinterpret_cast<f4 *>(a.seg_state + b.slot * seq_size + at + 32 * j + 4 * q) =
+                    *reinterpret_cast<const f4 *>(a.state + b.n * seq_size + at + 32 * j + 4 * q);
+        return;
+    }
     const int n_tok = b.n_tok;
     const TI *xrow = static_cast<const TI *>(a.xbc) + b.row * d.C;
     const TI *dtp = static_cast<const TI *>(a.dt) + b.row * d.dt_stride + b.h;
@@ -900,8 +948,8 @@ __global__ __launch_bounds__(256, 2) void ssm_end_kernel(SsmDims d, ScanArgsT a)
         for (int q = 0; q < 2; ++q) *reinterpret_cast<f4 *>(to + 32 * j + 4 * q) = MT::scaled ? S[j][q] * sdown : S[j][q];
 }
 
-// Over the segments of a sequence: the state each starts from replaces its own
-// end state, and the last one's end is the sequence's.  One float4 a thread.
+// Over the segments of a sequence: the state each starts from takes the place of
+// its own end state.  One float4 a thread.
 __global__ __launch_bounds__(256) void ssm_segment_kernel(SsmDims d, ScanArgsT a)
 {
     const int64_t n = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
@@ -923,7 +971,7 @@ __global__ __launch_bounds__(256) void ssm_segment_kernel(SsmDims d, ScanArgsT a
         float decay[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            const int64_t s = s0 + i < segs ? s0 + i : segs - 1;
+            const int64_t s = s0 + i < segs - 1 ? s0 + i : segs - 2;  // (the last has no end state here)
             own[i] = *reinterpret_cast<const f4 *>(p + s * seq_size);
             decay[i] = dec[s * d.H];
         }
@@ -934,20 +982,30 @@ __global__ __launch_bounds__(256) void ssm_segment_kernel(SsmDims d, ScanArgsT a
                 S = S * decay[i] + own[i];
             }
     }
-    if (a.state_out) *reinterpret_cast<f4 *>(a.state_out + n * seq_size + at) = S;
 }
 
-// Tokens of a segment, in whole batches of decays: as many as make the launch
-// about as many blocks as the chip's 256 CUs hold at once, two a CU.  Measured:
-// 2048 tokens of 64 heads, N = 128, bf16: 256 blocks 50 us, 512 45, 1024 44;
-// 27135 packed tokens: 530, 398, 420.
-int segment_tokens(const SsmDims &d)
+// Tokens of a segment, in whole chunks: as many as give the chip's 256 CUs two
+// blocks each, which hide one another's latency; where that would leave a block
+// 128 tokens or less, one block each, of at least 128.  A batch of sequences of
+// up to 256 tokens is not cut: two segments cost two more kernels' latency.
+// Measured, 64 heads of 64, N = 128, bf16, by blocks: 2048 tokens 256 50 us, 512
+// 45, 1024 44; 27135 packed tokens 530, 398, 420; 1024 tokens 256 31.6, 512
+// 34.7; 512 tokens 128 28.5, 256 22.6, 512 29; 256 tokens 64 17, 128 20.
+int segment_tokens(const SsmDims &d, int64_t max_T)
 {
-    const int64_t blocks = (int64_t)d.H * ((d.P + 63) / 64), room = 512;
-    int64_t tile = (d.T * blocks + room - 1) / room;
-    tile = (tile + BATCH - 1) / BATCH * BATCH;
-    return (int)(tile < BATCH ? BATCH : tile);
+    const int64_t all = d.T * d.H * ((d.P + 63) / 64);  // tokens of all blocks
+    auto share = [&](int64_t blocks) { return (all + blocks * 64 - 1) / (blocks * 64) * 64; };
+    int64_t tile = share(512);
+    if (tile <= 128) tile = share(256) < 128 ? 128 : share(256);
+    return (int)(max_T <= 256 && tile < 256 ? 256 : tile);
 }
+
+// Up to this many segments of a sequence the chunk kernel's blocks run over the
+// ones before theirs themselves, which costs them reads that grow with the
+// segments and saves a launch.  Measured against ssm_segment_kernel, as above:
+// 2 segments 28.9 and 32.4 us, 4 31.7 and 35.6, 7 35.5 and 37.2, 8 49.0 and 47.7
+// (fp16), 16 122 and 111.
+constexpr int JOIN_SEGMENTS = 7;
 
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -956,17 +1014,17 @@ size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 size_t ssm_scan_workspace_bytes(const gdn_ssm_shape &s)
 {
     const SsmDims d = ssm_dims(s);
-    const int tile = segment_tokens(d);
+    const int tile = segment_tokens(d, s.max_T);
     if (s.max_T <= tile) return 0;
     const size_t slots = (size_t)(d.T / tile + d.n_seq);
     return round256(slots * d.H * d.P * d.N * sizeof(float)) + round256(slots * d.H * sizeof(float));
 }
 
 template <typename TI, typename TO, int N>
-static void launch_scan_t(const SsmDims &d, const SsmScanArgs &a, bool segments, hipStream_t st)
+static void launch_scan_t(const SsmDims &d, const SsmScanArgs &a, bool segments, int64_t max_T, hipStream_t st)
 {
     constexpr int PARTS = sizeof(TI) == 4 ? 1 : Mat<TI>::scaled ? 2 : sizeof(TO) == 4 ? 3 : 2;
-    ScanArgsT t{a.cu, a.xbc, a.dt, a.A_log, a.dt_bias, a.D, a.state, a.state_out, a.y, nullptr, nullptr, segment_tokens(d)};
+    ScanArgsT t{a.cu, a.xbc, a.dt, a.A_log, a.dt_bias, a.D, a.state, a.state_out, a.y, nullptr, nullptr, segment_tokens(d, max_T), false, false};
     if (!segments) t.tile = 1 << 30;  // every sequence is one segment, whatever cu_seqlens holds
     const int64_t slots = d.T / t.tile + d.n_seq;
     const int pt_n = (d.P + 63) / 64;
@@ -977,19 +1035,22 @@ static void launch_scan_t(const SsmDims &d, const SsmScanArgs &a, bool segments,
     if (segments) {
         t.seg_state = static_cast<float *>(a.ws);
         t.seg_decay = reinterpret_cast<float *>(static_cast<char *>(a.ws) + round256((size_t)slots * d.H * d.P * N * sizeof(float)));
+        t.joined = max_T > (int64_t)JOIN_SEGMENTS * t.tile;
+        t.copied = !t.joined && a.state && a.state == a.state_out;
         hipLaunchKernelGGL((ssm_end_kernel<TI, N>), grid((int64_t)d.H * pt_n, slots), dim3(256), 0, st, d, t);
-        hipLaunchKernelGGL(ssm_segment_kernel, grid(((int64_t)d.H * d.P * N / 4 + 255) / 256, d.n_seq), dim3(256), 0, st, d, t);
+        if (t.joined)
+            hipLaunchKernelGGL(ssm_segment_kernel, grid(((int64_t)d.H * d.P * N / 4 + 255) / 256, d.n_seq), dim3(256), 0, st, d, t);
     }
     hipLaunchKernelGGL((ssm_chunk_kernel<TI, TO, N, PARTS>), grid((int64_t)d.H * pt_n, slots), dim3(256), 0, st, d, t);
 }
 
 template <typename TI, typename TO>
-static void launch_scan_n(const SsmDims &d, const SsmScanArgs &a, bool segments, hipStream_t st)
+static void launch_scan_n(const SsmDims &d, const SsmScanArgs &a, bool segments, int64_t max_T, hipStream_t st)
 {
-    if (d.N == 32) launch_scan_t<TI, TO, 32>(d, a, segments, st);
-    else if (d.N == 64) launch_scan_t<TI, TO, 64>(d, a, segments, st);
-    else if (d.N == 128) launch_scan_t<TI, TO, 128>(d, a, segments, st);
-    else launch_scan_t<TI, TO, 256>(d, a, segments, st);
+    if (d.N == 32) launch_scan_t<TI, TO, 32>(d, a, segments, max_T, st);
+    else if (d.N == 64) launch_scan_t<TI, TO, 64>(d, a, segments, max_T, st);
+    else if (d.N == 128) launch_scan_t<TI, TO, 128>(d, a, segments, max_T, st);
+    else launch_scan_t<TI, TO, 256>(d, a, segments, max_T, st);
 }
 
 hipError_t launch_ssm_scan(const gdn_ssm_shape &s, const SsmScanArgs &a, hipStream_t st)
@@ -997,8 +1058,8 @@ hipError_t launch_ssm_scan(const gdn_ssm_shape &s, const SsmScanArgs &a, hipStre
     const SsmDims d = ssm_dims(s);
     const bool segments = ssm_scan_workspace_bytes(s) > 0;
     GDN_SSM_IO(s.io_dtype,
-        if (s.out_dtype == GDN_F32) launch_scan_n<TI, float>(d, a, segments, st);
-        else launch_scan_n<TI, TI>(d, a, segments, st);)
+        if (s.out_dtype == GDN_F32) launch_scan_n<TI, float>(d, a, segments, s.max_T, st);
+        else launch_scan_n<TI, TI>(d, a, segments, s.max_T, st);)
     return hipGetLastError();
 }
 

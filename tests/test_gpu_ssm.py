@@ -166,6 +166,31 @@ def test_scan(gpu, io, out, lens, H, P, G, N):
     L.check_scan(y.t, S.t, out)
 
 
+# sequences of 1 to 9 segments of 128 tokens (2 heads), and of one of 256; the
+# last segment from 1 token to a whole one
+@pytest.mark.parametrize("io,N", [("f32", 32), ("f16", 128), ("bf16", 128), ("bf16", 256)])
+@pytest.mark.parametrize("lens", [[256], [257], [255, 256, 1], [512, 129, 0, 128], [7 * 128], [7 * 128 + 1],
+                                  [8 * 128], [9 * 128, 130, 384, 1]], ids=str)
+def test_scan_of_few_and_many_segments(gpu, io, N, lens):
+    L = Layer(lens, H=2, P=64, G=1, N=N, io=io, seed=11)
+    y, S = L.run_scan()
+    L.check_scan(y, S)
+    S2 = L.state.clone()  # state updated in place: bit for bit the same
+    y2, _ = L.run_scan(state=S2, state_out=S2)
+    assert torch.equal(y, y2) and torch.equal(S, S2)
+
+
+def test_scan_without_a_state_to_keep(gpu):
+    for lens in ([300, 40], [1200, 5], [37]):
+        L = Layer(lens, H=2, P=48, G=1, N=64, io="bf16", seed=12)
+        s = L.shape()
+        y, _ = L.run_scan()
+        y2 = torch.empty_like(y)
+        ws = torch.empty(max(256, ssm.gdn_ssm_scan_workspace_bytes(s)), dtype=torch.uint8, device="cuda")
+        ssm.gdn_ssm_scan(s, L.cu_t, L.xbc, L.dt, L.A_log, L.dt_bias, L.D, L.state, None, y2, ws)
+        assert torch.equal(y, y2)
+
+
 @pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
 def test_scan_options(gpu, io):
     L = Layer([100, 5], io=io)
