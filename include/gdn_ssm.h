@@ -64,8 +64,8 @@ extern "C" {
 
 /* Sizes of one call.  Supported: 1 <= groups, heads % groups == 0, heads <=
  * 4096; head_dim a multiple of 16 up to 256; state_dim 32, 64, 128 or 256;
- * conv_width 2, 3 or 4; out_dtype GDN_F32 or io_dtype; n_seq >= 1,
- * 0 <= max_T <= total_T <= 2^27;
+ * conv_width 2, 3 or 4; out_dtype GDN_F32 or io_dtype; 1 <= n_seq <= 2^20;
+ * 0 <= max_T <= total_T <= 2^27; strides 0 or a row's elements up to 2^40;
  * 0 <= dt_min <= dt_max (dt_max may be +infinity). */
 typedef struct gdn_ssm_shape {
     int32_t heads, head_dim, groups, state_dim;
@@ -99,7 +99,11 @@ int gdn_ssm_conv(const gdn_ssm_shape *shape, const int32_t *cu_seqlens, const vo
  *   S <- exp(-exp(A_log[h]) dt) S + dt x B^T
  *   y[t][h] = S C + D[h] x
  * The state, the decays and every sum are held in fp32 (sums of log decays in
- * 64 bits).  A decay below e^-200 is taken as e^-200, which is 0 in fp32.
+ * 64 bits).  A decay below e^-200 is taken as e^-200, which is 0 in fp32, and a
+ * token that the decays after it bring below e^-104 no longer counts.  Tokens are
+ * taken in chunks: a value that is not finite in x, B, C or dt makes outputs of
+ * its own sequence undefined from up to 63 tokens before it on (a channel of x:
+ * those of that channel alone); the other sequences are not touched by it.
  * In: cu_seqlens, xbc [total_T][C] dense (gdn_ssm_conv's output), dt, A_log,
  * dt_bias, D, state.  Out: y; state_out (NULL: not kept; may be state itself).
  * A sequence of no tokens keeps its state.

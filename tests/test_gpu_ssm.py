@@ -192,6 +192,31 @@ def test_scan_without_a_state_to_keep(gpu):
 
 
 @pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_values_that_are_not_finite_stay_in_their_sequence(gpu, io, bad):
+    # 2 heads of 32, the bad token 700 of the second sequence of 1000
+    L = Layer([130, 1000, 77], H=2, P=32, G=1, N=64, io=io, seed=13)
+    y0, S0 = L.run_scan()
+    at, n = 130 + 700, L.cu
+    clean = L.xbc.clone()
+    L.xbc[at, 32 + 5] = bad  # channel 5 of head 1
+    y, S = L.run_scan()
+    y0c, yc = y0.clone(), y.clone()
+    y0c[at - 63:n[2], 1, 5], yc[at - 63:n[2], 1, 5] = 0, 0
+    S0c, Sc = S0.clone(), S.clone()
+    S0c[1, 1, 5], Sc[1, 1, 5] = 0, 0
+    assert torch.equal(y0c, yc) and torch.equal(S0c, Sc)
+    assert not torch.isfinite(y[at, 1, 5]) and not torch.isfinite(S[1, 1, 5]).any()
+    L.xbc.copy_(clean)
+    L.xbc[at, 2 * 32 + 7] = bad  # B's value 7
+    y, S = L.run_scan()
+    for lo, hi in ((0, at - 63), (n[2], n[3])):
+        assert torch.equal(y0[lo:hi], y[lo:hi])
+    assert torch.equal(S0[0], S[0]) and torch.equal(S0[2], S[2])
+    assert not torch.isfinite(y[at]).any()
+
+
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
 def test_scan_options(gpu, io):
     L = Layer([100, 5], io=io)
     banner("gdn_ssm_scan without D and state", io)
