@@ -39,13 +39,13 @@
 //   fp32: one part, on the fp32 matrix instructions.
 //
 // Bound.  At 16 bits by what a wave can issue between the barriers of a chunk:
-// about 110 matrix instructions of 16 cycles and 550 others a wave and chunk of
-// 64 tokens at N = 128, which take 9000 cycles with two blocks on a CU; the
+// about 100 matrix instructions of 16 cycles and 550 vector ones a wave and chunk
+// of 64 tokens at N = 128, which take 9000 cycles with two blocks on a CU; the
 // matrix pipe is busy 27% of the time, HBM moves 1.7 TB/s.  fp32 is bound by the
 // rate of its matrix instructions, an eighth of the 16-bit one.  Measured, 64
 // heads of 64, N = 128: 2048 tokens bf16 45 us (end states 14, segments 8,
-// outputs 26; 190 TFLOP/s of matrix products), fp16 48, fp32 100; 27135 tokens in
-// 4 sequences bf16 331 us (85 + 246).
+// outputs 26), fp16 48, fp32 100; 27135 tokens in
+// 4 sequences bf16 331 us (end states 85).
 #include <type_traits>
 
 #include "ssm_device.h"
