@@ -44,7 +44,7 @@
 // matrix pipe is busy 27% of the time, HBM moves 1.7 TB/s.  fp32 is bound by the
 // rate of its matrix instructions, an eighth of the 16-bit one.  Measured, 64
 // heads of 64, N = 128: 2048 tokens bf16 45 us (end states 14, segments 8,
-// outputs 26), fp16 48, fp32 100; 27135 tokens in
+// outputs 26), fp16 48, fp32 98; 27135 tokens in
 // 4 sequences bf16 331 us (end states 85).
 #include <type_traits>
 
@@ -465,58 +465,60 @@ __global__ __launch_bounds__(256, N == 128 && PARTS == 3 ? 3 : 2) void ssm_chunk
     // in opposite order (tile t costs t + 1 products)
     const int mt = TT == 4 && ((b.slot * gridDim.x + blockIdx.x) >> 8 & 1) ? 3 - w : w;
 
-    // ---- M's rows t of tile T: D = B C^T has rows s, lane (g, t = c)
-    auto form_m = [&](auto tile, int bt) {
-        constexpr int T = decltype(tile)::value;
-        frag cf[J], bf[T + 1][J];
+    // ---- M's rows t of tile T, columns s of tiles FROM to TO - 1: D = B C^T has
+    // rows s, lane (g, t = c)
+    auto form_m = [&](auto tile, auto from, auto to, int bt) {
+        constexpr int T = decltype(tile)::value, FROM = decltype(from)::value, TO_ = decltype(to)::value, SN = TO_ - FROM;
+        constexpr int OFF = TO_ > T ? SN - 1 : SN;  // tiles below the diagonal
+        frag cf[J], bf[SN][J];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             cf[j] = row8(&sh.C[16 * T + c][32 * j + 8 * g]);
 #pragma unroll
-            for (int s = 0; s <= T; ++s) bf[s][j] = rowb(&sh.B[16 * s + c][0], j, g);
+            for (int s = 0; s < SN; ++s) bf[s][j] = rowb(&sh.B[16 * (FROM + s) + c][0], j, g);
         }
         const float2 lt = sh.lam[bt + 16 * T + c];
         const float Ft = sh.F[bt + 16 * T + c];
         float2 ls[4];
         float ds[4];
-        f4 Gs[T > 0 ? T : 1];
+        f4 Gs[OFF > 0 ? OFF : 1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             ls[i] = sh.lam[bt + 16 * T + 4 * g + i];
             ds[i] = sh.dt[bt + 16 * T + 4 * g + i];
         }
 #pragma unroll
-        for (int s = 0; s < T; ++s) Gs[s] = *reinterpret_cast<const f4 *>(&sh.G[T > 0 ? T - 1 : 0][bt + 16 * s + 4 * g]);
+        for (int s = 0; s < OFF; ++s) Gs[s] = *reinterpret_cast<const f4 *>(&sh.G[T > 0 ? T - 1 : 0][bt + 16 * (FROM + s) + 4 * g]);
         __builtin_amdgcn_sched_barrier(0);
-        f4 dd[T + 1];
+        f4 dd[SN];
 #pragma unroll
-        for (int s = 0; s <= T; ++s) dd[s] = f4(0.f);
+        for (int s = 0; s < SN; ++s) dd[s] = f4(0.f);
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int s = 0; s <= T; ++s) dd[s] = MT::mma(bf[s][j], cf[j], dd[s]);
+            for (int s = 0; s < SN; ++s) dd[s] = MT::mma(bf[s][j], cf[j], dd[s]);
         float most = 0.f;
 #pragma unroll
-        for (int s = 0; s < T; ++s) dd[s] = dd[s] * Gs[s] * Ft;
+        for (int s = 0; s < OFF; ++s) dd[s] = dd[s] * Gs[s] * Ft;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4 && OFF < SN; ++i) {
             const int si = 4 * g + i;
-            const float v = dd[T][i] * (exp_fast((lt.x - ls[i].x) + (lt.y - ls[i].y)) * ds[i]);
-            dd[T][i] = si < c ? v : si == c ? v + Dh : 0.f;
+            const float v = dd[SN - 1][i] * (exp_fast((lt.x - ls[i].x) + (lt.y - ls[i].y)) * ds[i]);
+            dd[SN - 1][i] = si < c ? v : si == c ? v + Dh : 0.f;
         }
         if (MT::scaled) {
 #pragma unroll
-            for (int s = 0; s <= T; ++s)
+            for (int s = 0; s < SN; ++s)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) most = fmaxf(most, fabsf(dd[s][i]));
             float up, down;
             scale_of(max_of_groups(most), up, down);
             if (g == 0) sh.mscale[16 * T + c] = down;
 #pragma unroll
-            for (int s = 0; s <= T; ++s) dd[s] *= up;
+            for (int s = 0; s < SN; ++s) dd[s] *= up;
         }
 #pragma unroll
-        for (int s = 0; s <= T; ++s) {
+        for (int s = 0; s < SN; ++s) {
             typedef TI t4 __attribute__((ext_vector_type(4)));
             const float v[4] = {dd[s][0], dd[s][1], dd[s][2], dd[s][3]};
             TI o[PARTS][4];
@@ -524,7 +526,7 @@ __global__ __launch_bounds__(256, N == 128 && PARTS == 3 ? 3 : 2) void ssm_chunk
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) {
                 const t4 q = {o[p][0], o[p][1], o[p][2], o[p][3]};
-                *reinterpret_cast<t4 *>(&sh.M[p][16 * T + c][16 * s + 4 * g]) = q;
+                *reinterpret_cast<t4 *>(&sh.M[p][16 * T + c][16 * (FROM + s) + 4 * g]) = q;
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -580,11 +582,23 @@ __global__ __launch_bounds__(256, N == 128 && PARTS == 3 ? 3 : 2) void ssm_chunk
         // product's loads: no load is given registers of an operand in use.
         f4 acc[TT];
         {
-            if (mt == 0) form_m(std::integral_constant<int, 0>{}, bt);
-            else if (mt == 1) form_m(std::integral_constant<int, 1>{}, bt);
-            else if (TT > 2) {
-                if (mt == 2) form_m(std::integral_constant<int, (TT > 2 ? 2 : 0)>{}, bt);
-                else form_m(std::integral_constant<int, (TT > 2 ? 3 : 0)>{}, bt);
+            constexpr std::integral_constant<int, 0> i0;
+            constexpr std::integral_constant<int, 1> i1;
+            constexpr std::integral_constant<int, 2> i2;
+            constexpr std::integral_constant<int, 3> i3;
+            constexpr std::integral_constant<int, 4> i4;
+            if constexpr (TT == 4) {
+                if (mt == 0) form_m(i0, i0, i1, bt);
+                else if (mt == 1) form_m(i1, i0, i2, bt);
+                else if (mt == 2) form_m(i2, i0, i3, bt);
+                else form_m(i3, i0, i4, bt);
+            } else if constexpr (MT::scaled) {  // a row's scale is that of all its columns
+                if (mt == 0) form_m(i0, i0, i1, bt);
+                else if (mt == 1) form_m(i1, i0, i2, bt);
+            } else {  // a tile a wave (2048 tokens fp32 100 -> 98 us)
+                if (w == 0) form_m(i0, i0, i1, bt);
+                else if (w == 1) form_m(i1, i0, i1, bt);
+                else if (w == 2) form_m(i1, i1, i2, bt);
             }
             __builtin_amdgcn_s_setprio(2);
             if (mine) {
