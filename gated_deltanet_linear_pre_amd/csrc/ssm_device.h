@@ -28,6 +28,19 @@ __device__ __forceinline__ void st16(T *p, typename Vec16<T>::type v)
     *reinterpret_cast<typename Vec16<T>::type *>(p) = v;
 }
 
+// 16 bytes at a uniform base and a 32-bit byte offset of the lane: one register
+// for the addresses of all rows a thread moves
+template <typename T>
+__device__ __forceinline__ typename Vec16<T>::type ld16_at(const T *base, uint32_t bytes)
+{
+    return ld16(reinterpret_cast<const T *>(reinterpret_cast<const char *>(base) + bytes));
+}
+template <typename T>
+__device__ __forceinline__ void st16_at(T *base, uint32_t bytes, typename Vec16<T>::type v)
+{
+    st16(reinterpret_cast<T *>(reinterpret_cast<char *>(base) + bytes), v);
+}
+
 // 8 consecutive elements widened to fp32, and narrowed (to nearest even) back
 template <typename T>
 __device__ __forceinline__ void load8f(const T *p, float (&x)[8])

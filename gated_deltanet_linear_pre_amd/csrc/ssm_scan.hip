@@ -346,14 +346,6 @@ __device__ __forceinline__ bool locate(const SsmDims &d, const ScanArgsT &a, Par
     return true;
 }
 
-// 16 bytes at a uniform base and a 32-bit byte offset of the lane: one register
-// for the addresses of all rows a thread moves
-template <typename T>
-__device__ __forceinline__ typename Vec16<T>::type ld16_at(const T *base, uint32_t bytes)
-{
-    return ld16(reinterpret_cast<const T *>(reinterpret_cast<const char *>(base) + bytes));
-}
-
 // The outputs of every segment, and the end state of the last one of a sequence.
 // PARTS: parts of S and M.
 template <typename TI, typename TO, int N, int PARTS>
