@@ -12,7 +12,7 @@
 // before its first store, so they are in flight together.  The four waves of
 // a block take four runs in turn of the same channels.  Measured: 27135 tokens of
 // 6144 bf16 channels 148 to 156 us, 4.3 to 4.5 TB/s, where a copy of 4 GB reaches
-// 4.76.
+// 4.76; 2048 of 4352 fp16 9.9 us, 3.6 TB/s, 3 us of it a launch.
 // History without a race when it is updated in place: only the run at a
 // sequence's first token reads the old history (later runs start K-1 or more
 // tokens in), and the same lanes write the new one after their reads.
