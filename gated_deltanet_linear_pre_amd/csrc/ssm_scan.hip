@@ -30,12 +30,14 @@
 //
 // Precision.  bf16 (and fp16, fp32) inputs enter the products as they are.  The
 // fp32 operands (S, M and the weighted x) are split into parts of the matrix
-// type whose products are summed in fp32:
-//   bf16: 3 parts (24 bits) for the state, and for S and M where y is fp32; 2
-//         parts (16 bits, an error of 2^-18 of each term) where y is bf16,
-//         whose own rounding is 2^-9;
-//   fp16: 2 parts (22 bits), scaled by a power of two to the largest value of
-//         the row or column that shares a contraction, as fp16's range asks;
+// type whose products are summed in fp32, whatever y's type:
+//   bf16: 3 parts, 24 bits.  (2 parts are off by up to 2^-17 of a term; where the
+//         terms cancel, y rounded to bf16 showed it: 0.2% of the outputs came out
+//         one step from those of an fp32 evaluation);
+//   fp16: 2 parts, off by at most 2^-23 of a value (an fp32 rounding: 2^-24) or
+//         2^-38 of the largest value of the row or column that shares a
+//         contraction, to which all are scaled by a power of two, as fp16's range
+//         asks.  That is below what the sums of an fp32 evaluation lose;
 //   fp32: one part, on the fp32 matrix instructions.
 //
 // Bound.  At 16 bits by what a wave can issue between the barriers of a chunk:
@@ -61,7 +63,7 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 template <typename T> struct Mat;
 template <> struct Mat<bf16> {
     typedef bf16 frag __attribute__((ext_vector_type(8)));
-    static constexpr int STATE_PARTS = 3;
+    static constexpr int PARTS = 3;
     static constexpr bool scaled = false;
     static __device__ __forceinline__ f4 mma(frag a, frag b, f4 c)
     {
@@ -70,7 +72,7 @@ template <> struct Mat<bf16> {
 };
 template <> struct Mat<_Float16> {
     typedef _Float16 frag __attribute__((ext_vector_type(8)));
-    static constexpr int STATE_PARTS = 2;
+    static constexpr int PARTS = 2;
     static constexpr bool scaled = true;
     static __device__ __forceinline__ f4 mma(frag a, frag b, f4 c)
     {
@@ -80,7 +82,7 @@ template <> struct Mat<_Float16> {
 // fp32: eight 4-deep products; product i contracts value i of every lane group
 template <> struct Mat<float> {
     typedef float frag __attribute__((ext_vector_type(8)));
-    static constexpr int STATE_PARTS = 1;
+    static constexpr int PARTS = 1;
     static constexpr bool scaled = false;
     static __device__ __forceinline__ f4 mma(frag a, frag b, f4 c)
     {
@@ -90,7 +92,7 @@ template <> struct Mat<float> {
     }
 };
 
-// Tokens of a chunk.  64 halve the times that S is split into operands; 32 leave
+// Tokens of a chunk; PARTS: those of M in LDS.  64 halve the times that S is split into operands; 32 leave
 // LDS for two blocks on a CU with N = 256 or fp32, and for three with three
 // parts of S and M.  Measured: N = 256, bf16 to fp32, 2005 tokens of 32 heads of
 // 128: 92 us by 32, 101 by 64; N = 128, 2048 tokens of 64 heads of 64, bf16 to
@@ -347,14 +349,14 @@ __device__ __forceinline__ bool locate(const SsmDims &d, const ScanArgsT &a, Par
 }
 
 // The outputs of every segment, and the end state of the last one of a sequence.
-// PARTS: parts of S and M.
-template <typename TI, typename TO, int N, int PARTS>
-__global__ __launch_bounds__(256, N == 128 && PARTS == 3 ? 3 : 2) void ssm_chunk_kernel(SsmDims d, ScanArgsT a)
+template <typename TI, typename TO, int N>
+__global__ __launch_bounds__(256, N == 128 && Mat<TI>::PARTS == 3 ? 3 : 2) void ssm_chunk_kernel(SsmDims d, ScanArgsT a)
 {
     typedef Mat<TI> MT;
     typedef typename MT::frag frag;
+    constexpr int PARTS = MT::PARTS;
     typedef ScanShared<TI, N, PARTS> Shared;
-    constexpr int Q = chunk_tokens<TI, N, PARTS>(), SP = MT::STATE_PARTS, J = N / 32, TT = Q / 16, KK = Q / 32;
+    constexpr int Q = chunk_tokens<TI, N, PARTS>(), J = N / 32, TT = Q / 16, KK = Q / 32;
     constexpr int V = Vec16<TI>::n;
     typedef typename Vec16<TI>::type vec;
     constexpr int NB = Q * N / V / 256;  // vectors of B (and C) a thread moves
@@ -670,9 +672,9 @@ __global__ __launch_bounds__(256, N == 128 && PARTS == 3 ? 3 : 2) void ssm_chunk
 #pragma unroll
                         for (int i = 0; i < 8; ++i) u[k][i] *= up;
                 }
-                frag uf[KK][SP];
+                frag uf[KK][PARTS];
 #pragma unroll
-                for (int k = 0; k < KK; ++k) split8<TI, SP>(u[k], uf[k]);
+                for (int k = 0; k < KK; ++k) split8<TI, PARTS>(u[k], uf[k]);
                 __builtin_amdgcn_sched_barrier(0);
                 // (in two parts of n, which bounds the registers: at N = 128 all
                 // of B^T at once spilled some, and 430 us on the packed batch
@@ -693,7 +695,7 @@ __global__ __launch_bounds__(256, N == 128 && PARTS == 3 ? 3 : 2) void ssm_chunk
 #pragma unroll
                     for (int k = 0; k < KK; ++k)
 #pragma unroll
-                        for (int p = 0; p < SP; ++p)
+                        for (int p = 0; p < PARTS; ++p)
 #pragma unroll
                             for (int j = 0; j < JS; ++j)
 #pragma unroll
@@ -785,7 +787,8 @@ __global__ __launch_bounds__(256, 2) void ssm_end_kernel(SsmDims d, ScanArgsT a)
     typedef Mat<TI> MT;
     typedef typename MT::frag frag;
     typedef EndShared<TI, N> Shared;
-    constexpr int Q = chunk_tokens<TI, N, 1>(), SP = MT::STATE_PARTS, J = N / 32, KK = Q / 32;
+    constexpr int PARTS = MT::PARTS;
+    constexpr int Q = chunk_tokens<TI, N, 1>(), J = N / 32, KK = Q / 32;
     constexpr int V = Vec16<TI>::n, NB = Q * N / V / 256, NX = Q * 64 / V / 256;
     constexpr int RB = 256 * V / N, RX = 256 * V / 64;
     // products accumulate onto S itself, all of B^T's operands at once (fp16
@@ -926,9 +929,9 @@ __global__ __launch_bounds__(256, 2) void ssm_end_kernel(SsmDims d, ScanArgsT a)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) u[k][i] *= up;
             }
-            frag uf[KK][SP];
+            frag uf[KK][PARTS];
 #pragma unroll
-            for (int k = 0; k < KK; ++k) split8<TI, SP>(u[k], uf[k]);
+            for (int k = 0; k < KK; ++k) split8<TI, PARTS>(u[k], uf[k]);
 #pragma unroll
             for (int j0 = 0; j0 < J; j0 += JS) {
                 if (j0) load_b(j0);
@@ -941,7 +944,7 @@ __global__ __launch_bounds__(256, 2) void ssm_end_kernel(SsmDims d, ScanArgsT a)
 #pragma unroll
                 for (int k = 0; k < KK; ++k)
 #pragma unroll
-                    for (int p = 0; p < SP; ++p)
+                    for (int p = 0; p < PARTS; ++p)
 #pragma unroll
                         for (int j = 0; j < JS; ++j)
 #pragma unroll
@@ -1041,7 +1044,6 @@ size_t ssm_scan_workspace_bytes(const gdn_ssm_shape &s)
 template <typename TI, typename TO, int N>
 static void launch_scan_t(const SsmDims &d, const SsmScanArgs &a, bool segments, int64_t max_T, hipStream_t st)
 {
-    constexpr int PARTS = sizeof(TI) == 4 ? 1 : Mat<TI>::scaled ? 2 : sizeof(TO) == 4 ? 3 : 2;
     ScanArgsT t{a.cu, a.xbc, a.dt, a.A_log, a.dt_bias, a.D, a.state, a.state_out, a.y, nullptr, nullptr, segment_tokens(d, max_T), false, false};
     if (!segments) t.tile = 1 << 30;  // every sequence is one segment, whatever cu_seqlens holds
     const int64_t slots = d.T / t.tile + d.n_seq;
@@ -1059,7 +1061,7 @@ static void launch_scan_t(const SsmDims &d, const SsmScanArgs &a, bool segments,
         if (t.joined)
             hipLaunchKernelGGL(ssm_segment_kernel, grid(((int64_t)d.H * d.P * N / 4 + 255) / 256, d.n_seq), dim3(256), 0, st, d, t);
     }
-    hipLaunchKernelGGL((ssm_chunk_kernel<TI, TO, N, PARTS>), grid((int64_t)d.H * pt_n, slots), dim3(256), 0, st, d, t);
+    hipLaunchKernelGGL((ssm_chunk_kernel<TI, TO, N>), grid((int64_t)d.H * pt_n, slots), dim3(256), 0, st, d, t);
 }
 
 template <typename TI, typename TO>

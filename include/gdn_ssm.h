@@ -99,7 +99,10 @@ int gdn_ssm_conv(const gdn_ssm_shape *shape, const int32_t *cu_seqlens, const vo
  *   S <- exp(-exp(A_log[h]) dt) S + dt x B^T
  *   y[t][h] = S C + D[h] x
  * The state, the decays and every sum are held in fp32 (sums of log decays in
- * 64 bits).  A decay below e^-200 is taken as e^-200, which is 0 in fp32, and a
+ * 64 bits), whatever out_dtype is.  As operands of the matrix products the fp32
+ * quantities keep all of their bits where io is fp32 or bf16; where it is fp16
+ * they are off by at most 2^-23 of their value or 2^-38 of the largest of their
+ * row or column.  A decay below e^-200 is taken as e^-200, which is 0 in fp32, and a
  * token that the decays after it bring below e^-104 no longer counts.  Tokens are
  * taken in chunks: a value that is not finite in x, B, C or dt makes outputs of
  * its own sequence undefined from up to 63 tokens before it on (a channel of x:
