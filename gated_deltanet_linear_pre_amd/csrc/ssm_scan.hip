@@ -1005,6 +1005,8 @@ __global__ __launch_bounds__(256) void ssm_segment_kernel(SsmDims d, ScanArgsT a
     }
 }
 
+constexpr int NO_SEGMENTS = 1 << 30;  // tokens: more than a call may have
+
 // Tokens of a segment, in whole chunks: as many as give the chip's 256 CUs two
 // blocks each, which hide one another's latency; where that would leave a block
 // 128 tokens or less, one block each, of at least 128.  A batch of sequences of
@@ -1018,7 +1020,9 @@ int segment_tokens(const SsmDims &d, int64_t max_T)
     auto share = [&](int64_t blocks) { return (all + blocks * 64 - 1) / (blocks * 64) * 64; };
     int64_t tile = share(512);
     if (tile <= 128) tile = share(256) < 128 ? 128 : share(256);
-    return (int)(max_T <= 256 && tile < 256 ? 256 : tile);
+    if (max_T <= 256 && tile < 256) tile = 256;
+    // (at the ends of the sizes a share passes 32 bits; no sequence is that long)
+    return tile < NO_SEGMENTS ? (int)tile : NO_SEGMENTS;
 }
 
 // Up to this many segments of a sequence the chunk kernel's blocks run over the
@@ -1045,7 +1049,7 @@ template <typename TI, typename TO, int N>
 static void launch_scan_t(const SsmDims &d, const SsmScanArgs &a, bool segments, int64_t max_T, hipStream_t st)
 {
     ScanArgsT t{a.cu, a.xbc, a.dt, a.A_log, a.dt_bias, a.D, a.state, a.state_out, a.y, nullptr, nullptr, segment_tokens(d, max_T), false, false};
-    if (!segments) t.tile = 1 << 30;  // every sequence is one segment, whatever cu_seqlens holds
+    if (!segments) t.tile = NO_SEGMENTS;  // every sequence is one segment, whatever cu_seqlens holds
     const int64_t slots = d.T / t.tile + d.n_seq;
     const int pt_n = (d.P + 63) / 64;
     auto grid = [](int64_t x, int64_t yz) {
