@@ -154,26 +154,31 @@ __device__ __forceinline__ Mat<float>::frag row8<float>(const float *p)
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// A 16-byte vector of a row of B (columns col..) to its places (see ScanShared)
+// 4 values of a row of B, whose rows start on 8 bytes (see ScanShared)
+template <typename T> struct BQuad {
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    typedef t4 type __attribute__((aligned(8)));
+};
+// A 16-byte vector of a row of B (columns col..) to its places
 __device__ __forceinline__ void store_b(float *row, int col, Vec16<float>::type v)
 {
-    *reinterpret_cast<f4 *>(row + (col & ~31) + (col & 4) * 4 + (col & 24) / 2) = v;
+    *reinterpret_cast<BQuad<float>::type *>(row + (col & ~31) + (col & 4) * 4 + (col & 24) / 2) = v;
 }
 template <typename T>
 __device__ __forceinline__ void store_b(T *row, int col, typename Vec16<T>::type v)
 {
-    typedef T t4 __attribute__((ext_vector_type(4)));
+    typedef typename BQuad<T>::type quad;
     T *p = row + (col & ~31) + (col & 24) / 2;
-    *reinterpret_cast<t4 *>(p) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
-    *reinterpret_cast<t4 *>(p + 16) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+    *reinterpret_cast<quad *>(p) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+    *reinterpret_cast<quad *>(p + 16) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
 }
 // n = 32j + 8g + 0..7 of a permuted row of B
 template <typename T>
 __device__ __forceinline__ typename Mat<T>::frag rowb(const T *row, int j, int g)
 {
-    typedef T t4 __attribute__((ext_vector_type(4)));
-    typedef t4 t4a __attribute__((aligned(8)));
-    const t4 a = *reinterpret_cast<const t4a *>(row + 32 * j + 4 * g), b = *reinterpret_cast<const t4a *>(row + 32 * j + 16 + 4 * g);
+    typedef typename BQuad<T>::type quad;
+    const typename BQuad<T>::t4 a = *reinterpret_cast<const quad *>(row + 32 * j + 4 * g);
+    const typename BQuad<T>::t4 b = *reinterpret_cast<const quad *>(row + 32 * j + 16 + 4 * g);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -282,6 +287,8 @@ constexpr int BATCH = 256;  // tokens whose decays are formed at a time, one a t
 template <typename TI, int N, int PARTS> struct __attribute__((aligned(16))) ScanShared {
     static constexpr int Q = chunk_tokens<TI, N, PARTS>(), E16 = 16 / sizeof(TI), REFS = Q / 16 - 1;
     static constexpr int BP = N + 40 / sizeof(TI), CP = N + 2 * E16, XP = 64 + 2 * E16, MP = Q + E16;
+    static_assert(BP * sizeof(TI) % alignof(typename BQuad<TI>::type) == 0, "rows of B start where its vectors may");
+    static_assert(CP * sizeof(TI) % 16 == 0 && XP * sizeof(TI) % 16 == 0 && MP * sizeof(TI) % 16 == 0, "16-byte vectors");
     TI C[Q][CP];
     TI X[Q][XP];
     TI M[PARTS][Q][MP];
