@@ -208,6 +208,36 @@ __device__ __forceinline__ Mat<float>::frag col8<float>(const float *base, int p
     return v;
 }
 
+// ---- values that are not finite: all bits of the exponent set ----------------
+template <typename T> struct Bits {
+    typedef unsigned short u;
+    static constexpr unsigned short INF = std::is_same<T, _Float16>::value ? 0x7C00 : 0x7F80, VALUE = 0x7FFF;
+};
+template <> struct Bits<float> {
+    typedef unsigned u;
+    static constexpr unsigned INF = 0x7F800000, VALUE = 0x7FFFFFFF;
+};
+template <typename T, int KK>
+__device__ __forceinline__ bool any_not_finite(const typename Mat<T>::frag (&x)[KK])
+{
+    typedef typename Bits<T>::u u;
+    typedef u u2 __attribute__((ext_vector_type(2)));
+    typedef u u8 __attribute__((ext_vector_type(8)));
+    u2 most = u2(0);
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+        const u8 b = __builtin_bit_cast(u8, x[k]) & Bits<T>::VALUE;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) most = __builtin_elementwise_max(most, u2{b[i], b[i + 1]});
+    }
+    return most[0] >= Bits<T>::INF || most[1] >= Bits<T>::INF;
+}
+template <typename T>
+__device__ __forceinline__ bool not_finite(T v)
+{
+    return (__builtin_bit_cast(typename Bits<T>::u, v) & Bits<T>::VALUE) >= Bits<T>::INF;
+}
+
 // Power of two that brings `most` (>= 0) to 2^13..2^14, at most 2^40 (smaller
 // values than 2^-26 keep an error of 2^-65), and its inverse: products with
 // it are exact.  Non-finite values stay so.
@@ -732,6 +762,26 @@ __global__ __launch_bounds__(256, N == 128 && Mat<TI>::PARTS == 3 ? 3 : 2) void 
                             for (int p = 0; p < PARTS; ++p) mf[p][t][k] = row8(&sh.M[p][16 * t + c][32 * k + 8 * g]);
                         }
                 }
+                // A value of x that is not finite would meet M's zeros above the
+                // diagonal, and be NaN in the tokens before its own.  It is left
+                // out of the product, and its channel's outputs from it on are NaN.
+                const bool odd = __builtin_amdgcn_ballot_w64(any_not_finite<TI, KK>(xf)) != 0;
+                unsigned from = 0;  // the place of the first such value in channels p = 4g..4g+3, a byte each
+                if (odd) {
+                    int first = Q;  // of channel p = c
+#pragma unroll
+                    for (int k = KK - 1; k >= 0; --k)
+#pragma unroll
+                        for (int i = 7; i >= 0; --i)
+                            if (not_finite<TI>(xf[k][i])) {
+                                first = 32 * k + 8 * g + i;
+                                xf[k][i] = TI(0);
+                            }
+                    first = min(first, __shfl_xor(first, 16, 64));
+                    first = min(first, __shfl_xor(first, 32, 64));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) from |= (unsigned)__shfl(first, 4 * g + i, 64) << 8 * i;
+                }
                 __builtin_amdgcn_sched_barrier(0);
                 f4 z[TT];
 #pragma unroll
@@ -742,6 +792,12 @@ __global__ __launch_bounds__(256, N == 128 && Mat<TI>::PARTS == 3 ? 3 : 2) void 
                     for (int p = 0; p < PARTS; ++p)
 #pragma unroll
                         for (int t = 2 * k; t < TT; ++t) z[t] = MT::mma(xf[k], mf[p][t][k], z[t]);
+                if (odd) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int t = 0; t < TT; ++t) z[t][i] = 16 * t + c >= (int)(from >> 8 * i & 0xFF) ? __builtin_nanf("") : z[t][i];
+                }
                 char *yp = reinterpret_cast<char *>(static_cast<TO *>(a.y) + ((b.row + t0) * d.H + h) * d.P + p0);
                 typedef TO o4 __attribute__((ext_vector_type(4)));
                 o4 o[TT];

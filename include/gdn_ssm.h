@@ -103,10 +103,10 @@ int gdn_ssm_conv(const gdn_ssm_shape *shape, const int32_t *cu_seqlens, const vo
  * quantities keep all of their bits where io is fp32 or bf16; where it is fp16
  * they are off by at most 2^-23 of their value or 2^-38 of the largest of their
  * row or column.  A decay below e^-200 is taken as e^-200, which is 0 in fp32, and a
- * token that the decays after it bring below e^-104 no longer counts.  Tokens are
- * taken in chunks: a value that is not finite in x, B, C or dt makes outputs of
- * its own sequence undefined from up to 63 tokens before it on (a channel of x:
- * those of that channel alone); the other sequences are not touched by it.
+ * token that the decays after it bring below e^-104 no longer counts.  A value
+ * that is not finite leaves every output before its token and every other sequence
+ * as they are; from its token on it makes outputs undefined: x those of its channel,
+ * dt those of its head, B those of its group's heads, C its token's of that group.
  * In: cu_seqlens, xbc [total_T][C] dense (gdn_ssm_conv's output), dt, A_log,
  * dt_bias, D, state.  Out: y; state_out (NULL: not kept; may be state itself).
  * A sequence of no tokens keeps its state.

@@ -26,3 +26,42 @@ def test_the_output_type_changes_the_last_rounding_only(gpu, io, N):
     lo, hi = (torch.nextafter(y32, torch.full_like(y32, v)).to(DT[io]) for v in (-np.inf, np.inf))
     wrong = int(((y < lo) | (y > hi) | (y != y)).sum())
     assert not wrong, f"{wrong} of {y.numel()} outputs rounded from something else"
+
+
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("N", [64, 128, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_value_that_is_not_finite_leaves_the_tokens_before_it(gpu, io, N, bad):
+    # one bad value of x, B, C or dt at places all over a chunk, in the first
+    # segment and in a later one: outputs before it, of other sequences and (x, dt)
+    # of other channels or heads are bit for bit those of the clean inputs
+    H, P = 4, 64
+    L = Layer([130, 600, 77], H=H, P=P, G=2, N=N, io=io, seed=22)
+    L.A_log.fill_(-3.0)  # decays that keep the value in the state to the end
+    clean_x, clean_dt = L.xbc.clone(), L.dt.clone()
+    for out in sorted({io, "f32"}):
+        L.xbc.copy_(clean_x), L.dt.copy_(clean_dt)
+        y0, S0 = L.run_scan(out)
+        banner("not finite", io, out, N, bad)
+        for t in (0, 1, 17, 31, 32, 47, 63, 64, 300, 511, 575, 599):
+            at, end = 130 + t, 730
+            for what, col in (("x", 2 * P + 37), ("B", H * P + 5), ("C", H * P + 2 * N + N + 9), ("dt", 3)):
+                L.xbc.copy_(clean_x), L.dt.copy_(clean_dt)
+                (L.dt if what == "dt" else L.xbc)[at, col] = bad
+                y, S = L.run_scan(out)
+                same = y == y0
+                assert same[:at].all() and same[end:].all(), (what, t)
+                assert torch.equal(S[0], S0[0]) and torch.equal(S[2], S0[2])
+                if what == "x":
+                    same[at:end, 2, 37] = True
+                    assert not torch.isfinite(y[at, 2, 37]) and not torch.isfinite(S[1, 2, 37]).any()
+                elif what == "dt":
+                    same[at:end, 3] = True
+                    assert not torch.isfinite(y[at, 3]).any()
+                elif what == "B":
+                    same[at:end, :2] = True
+                    assert not torch.isfinite(y[at, :2]).any()
+                else:
+                    same[at, 2:] = True
+                    assert not torch.isfinite(y[at, 2:]).any()
+                assert same.all(), (what, t)
