@@ -238,15 +238,27 @@ __device__ __forceinline__ bool not_finite(T v)
     return (__builtin_bit_cast(typename Bits<T>::u, v) & Bits<T>::VALUE) >= Bits<T>::INF;
 }
 
+// the inverse of a power of two
+__device__ __forceinline__ float inverse(float x) { return __int_as_float((254 << 23) - __float_as_int(x)); }
 // Power of two that brings `most` (>= 0) to 2^13..2^14, at most 2^40 (smaller
 // values than 2^-26 keep an error of 2^-65), and its inverse: products with
 // it are exact.  Non-finite values stay so.
 __device__ __forceinline__ void scale_of(float most, float &up, float &down)
 {
-    int k = 14 - __builtin_amdgcn_frexp_expf(most);
-    k = k < -100 ? -100 : k > 40 ? 40 : k;
+    int k = 14 - __builtin_amdgcn_frexp_expf(most);  // (-114 at least)
+    k = k > 40 ? 40 : k;
     up = __int_as_float((127 + k) << 23);
-    down = __int_as_float((127 - k) << 23);
+    down = inverse(up);
+}
+// The same for the x that S gathers, whose scale S takes: at most 2^86 / size, with
+// S below 2^14 size, so that a scaled S stays below 2^100.  (size is a power of two;
+// up to 2^46, S up to 2^60, nothing is held back.)
+__device__ __forceinline__ void scale_beside(float most, float size, float &up, float &down)
+{
+    scale_of(most, up, down);
+    const float cap = __uint_as_float((340u << 23) - __float_as_uint(fmaxf(size, 0x1p46f)));
+    up = fminf(up, cap);
+    down = inverse(up);
 }
 // the largest of the four lanes that share lane & 15 (x >= 0): a lane-half
 // swap of x with itself leaves the two halves' values side by side, and a
@@ -612,6 +624,7 @@ __global__ __launch_bounds__(256, N == 128 && Mat<TI>::PARTS == 3 ? 3 : 2) void 
         // matrix instructions, and its results are taken before the next
         // product's loads: no load is given registers of an operand in use.
         f4 acc[TT];
+        float down = 1.f;  // fp16: the largest value of S's row p = c is below 2^14 down
         {
             constexpr std::integral_constant<int, 0> i0;
             constexpr std::integral_constant<int, 1> i1;
@@ -645,7 +658,8 @@ __global__ __launch_bounds__(256, N == 128 && Mat<TI>::PARTS == 3 ? 3 : 2) void 
                     acc[t] = f4(0.f);
                     e[t] = sh.E[bt + 16 * t + c];
                 }
-                float up = 1.f, down = 1.f, rdown[4] = {1.f, 1.f, 1.f, 1.f};
+                float up = 1.f, rdown[4] = {1.f, 1.f, 1.f, 1.f};
+                down = 1.f;
                 if (MT::scaled) {
                     float most = 0.f;
 #pragma unroll
@@ -702,7 +716,7 @@ __global__ __launch_bounds__(256, N == 128 && Mat<TI>::PARTS == 3 ? 3 : 2) void 
 #pragma unroll
                         for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(u[k][i]));
                     alpha *= sdown;
-                    scale_of(max_of_groups(most), up, sdown);
+                    scale_beside(max_of_groups(most), down, up, sdown);
                     alpha *= up;
 #pragma unroll
                     for (int k = 0; k < KK; ++k)
@@ -912,7 +926,7 @@ __global__ __launch_bounds__(256, 2) void ssm_end_kernel(SsmDims d, ScanArgsT a)
     f4 S[J][2];
 #pragma unroll
     for (int j = 0; j < J; ++j) S[j][0] = S[j][1] = f4(0.f);
-    float sdown = 1.f;
+    float sdown = 1.f, largest = 0.f;  // largest: of u in row p = c so far
     const float neg_a = -expf(a.A_log[b.h]), dt_bias = a.dt_bias[b.h];
     double after = 0.0, all = 0.0;  // log decay after this batch, and of it
     float rest[4];                  // log decay after each 64 tokens of it
@@ -985,7 +999,11 @@ __global__ __launch_bounds__(256, 2) void ssm_end_kernel(SsmDims d, ScanArgsT a)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(u[k][i]));
                 scale = sdown;
-                scale_of(max_of_groups(most), up, sdown);
+                // |S| <= tokens max|u| max|B|, below 2^27 2^(e + 1) 2^16 with 2^e <= max|u|
+                most = max_of_groups(most);
+                largest = fmaxf(largest, most);
+                const float power = __uint_as_float(__float_as_uint(largest) & 0x7F800000u);
+                scale_beside(most, fminf(power, 0x1p84f) * 0x1p30f, up, sdown);
                 scale *= up;
 #pragma unroll
                 for (int k = 0; k < KK; ++k)

@@ -65,3 +65,29 @@ def test_a_value_that_is_not_finite_leaves_the_tokens_before_it(gpu, io, N, bad)
                     same[at, 2:] = True
                     assert not torch.isfinite(y[at, 2:]).any()
                 assert same.all(), (what, t)
+
+
+def test_fp16_scan_of_a_state_far_above_its_inputs(gpu):
+    # states of 2^100 that hardly decay, then inputs that are the smallest of fp16:
+    # everything stays inside fp32's range, so does the scan
+    for lens in ([200, 3], [700]):
+        L = Layer(lens, H=2, G=1, io="f16", seed=23)
+        L.state *= 2.0 ** 100
+        L.A_log.fill_(-12.0)
+        L.xbc[:, :2 * 64] *= 2.0 ** -22
+        banner("gdn_ssm_scan of large states", lens)
+        y, S = L.run_scan("f32")
+        L.check_scan(y, S, "f32")
+
+
+def test_fp16_scan_of_steps_far_above_one(gpu):
+    # steps of 1e19 with decays of e^-1.35 a token: what the last 64 tokens of a
+    # segment of 128 leave in its state is 2^124 times what the first ones do
+    L = Layer([900, 40], H=2, P=64, G=1, io="f16", seed=24)
+    L.dt_bias.fill_(1e19)
+    L.A_log.fill_(-43.45)
+    L.xbc[:, :2 * 64 + 128] *= 1e4
+    assert L.xbc.isfinite().all()
+    banner("gdn_ssm_scan of large steps")
+    y, S = L.run_scan("f32")
+    L.check_scan(y, S, "f32")
