@@ -2,14 +2,17 @@
 
 Same manner as binding.py: the C names, tensors become device pointers, the
 stream defaults to torch's current stream, a non-zero status raises GdnError.
-None stands for the optional buffers.  A tensor that is not on the current HIP
-device is refused here (the library sees addresses only); everything else is
-checked by the library.  Rows of the raw xbc and of dt may be column blocks of
-a wider tensor: pass the view and its stride(0) in the shape.
+None stands for the optional buffers.  The library sees addresses only, so what
+they stand for is checked here: a tensor has to be on the current HIP device, of
+the type that the shape names, with elements enough for it and without gaps
+(ValueError otherwise).  Rows of the raw xbc, of dt and of the norm's x and z may
+be column blocks of a wider tensor: pass the view and its stride(0) in the shape.
+Addresses given as integers are not checked.  Everything else is the library's.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -79,9 +82,66 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-_current_device = torch.cuda.current_device
-# the address torch.cuda.current_stream().cuda_stream holds, without the stream
-# object around it (2.8 us of a call's 8)
+_TORCH = {GDN_F32: torch.float32, GDN_F16: torch.float16, GDN_BF16: torch.bfloat16}
+
+
+@functools.lru_cache(maxsize=256)
+def _plan(name: str, raw: bytes):
+    """(argument, type, elements, strides, size) of a call's tensors, from the bytes
+    of its shape.  strides None: a tensor without gaps, of that many elements."""
+    def flat(arg, dtype, least):
+        return arg, dtype, least, None, None
+
+    def rows(arg, dtype, n, cols, stride):
+        return arg, dtype, None, (stride or cols, 1), (n, cols)
+
+    i32, f32 = torch.int32, torch.float32
+    if name == "gdn_group_norm":
+        s = gdn_norm_shape.from_buffer_copy(raw)
+        io, ch = _TORCH.get(s.io_dtype), s.channels
+        return (rows("x", _TORCH.get(s.x_dtype), s.rows, ch, s.x_stride), rows("z", io, s.rows, ch, s.z_stride),
+                flat("weight", io, ch), flat("bias", io, ch), flat("y", io, s.rows * ch))
+    s = gdn_ssm_shape.from_buffer_copy(raw)
+    H, T, io, out = s.heads, s.total_T, _TORCH.get(s.io_dtype), _TORCH.get(s.out_dtype)
+    x = H * s.head_dim
+    C = x + 2 * s.groups * s.state_dim
+    cu, w, b = flat("cu_seqlens", i32, s.n_seq + 1), flat("conv_w", io, C * s.conv_width), flat("conv_b", io, C)
+    raw_x, dt = rows("xbc", io, T, C, s.xbc_stride), rows("dt", io, T, H, s.dt_stride)
+    heads = tuple(flat(k, f32, H) for k in ("A_log", "dt_bias", "D"))
+    hist = tuple(flat(k, io, s.n_seq * (s.conv_width - 1) * C) for k in ("hist", "hist_out"))
+    state = tuple(flat(k, f32, s.n_seq * x * s.state_dim) for k in ("state", "state_out"))
+    y = flat("y", out, T * x)
+    if name == "gdn_ssm_conv":
+        return (cu, raw_x, w, b, *hist, flat("out", io, T * C))
+    if name == "gdn_ssm_scan":
+        return (cu, flat("xbc", io, T * C), dt, *heads, *state, y, flat("workspace", None, 0))
+    return (raw_x, w, b, dt, *heads, *hist, *state, y)
+
+
+def _refuse(name: str, x, arg, dtype, least, strides, size):
+    """ValueError if `x` is not the tensor of this entry of the plan; _call comes
+    here with what is not so at first sight."""
+    if dtype is not None and x.dtype is not dtype:
+        raise ValueError(f"{name}: {arg} is {x.dtype}, the shape says {dtype}")
+    if strides is None:
+        if not x.is_contiguous():
+            raise ValueError(f"{name}: {arg} has gaps between its elements (strides {x.stride()})")
+        if x.numel() < least:
+            raise ValueError(f"{name}: {arg} has {x.numel()} elements of {least}")
+        return
+    n, cols = size
+    if x.is_contiguous():
+        fits = n <= 0 or x.numel() >= (n - 1) * strides[0] + cols
+    else:
+        fits = x.dim() == 2 and x.shape[0] >= n and x.shape[1] >= cols and x.stride(1) == 1 and (n <= 1 or x.stride(0) == strides[0])
+    if not fits:
+        raise ValueError(f"{name}: {arg} of {tuple(x.shape)}, strides {x.stride()}, is not {n} rows of {cols} elements, {strides[0]} apart")
+
+
+# torch.cuda.current_device() without its look at whether torch has started (0.2 us),
+# which a tensor on a device answers, and the address torch.cuda.current_stream()
+# holds without the stream object around it (2.8 us of a call's 8)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -95,10 +155,13 @@ def _call(name: str, shape, tensors, tail, stream, check: bool) -> int:
     """One library call: addresses, then `tail`, then the stream."""
     dev = -1
     args = []
-    for x in tensors:
+    for x, (arg, dtype, least, strides, size) in zip(tensors, _plan(name, bytes(shape))):
         if x is None or isinstance(x, int):
             args.append(x)
             continue
+        if x.dtype is not dtype or not (x.is_contiguous() and x.numel() >= least if strides is None
+                                        else x.shape == size and x.stride() == strides):
+            _refuse(name, x, arg, dtype, least, strides, size)
         at = x.get_device()
         if at != dev or at < 0:
             if at < 0:
@@ -108,7 +171,7 @@ def _call(name: str, shape, tensors, tail, stream, check: bool) -> int:
                 raise ValueError(f"{name}: a tensor on {x.device}, but the current HIP device is {dev}")
         args.append(x.data_ptr())
     if stream is None or not isinstance(stream, int):
-        stream = _stream(stream, dev if dev >= 0 else _current_device())
+        stream = _stream(stream, dev if dev >= 0 else torch.cuda.current_device())
     st = getattr(_lib or lib(), name)(ctypes.byref(shape), *args, *tail, stream)
     if check and st != 0:
         raise GdnError(name, st)
@@ -127,8 +190,11 @@ def gdn_ssm_scan_workspace_bytes(shape) -> int:
 
 def gdn_ssm_scan(shape, cu_seqlens, xbc, dt, A_log, dt_bias, D, state, state_out, y,
                  workspace=None, workspace_bytes=None, stream=None, check=True) -> int:
+    held = workspace.nbytes if isinstance(workspace, torch.Tensor) else 0
     if workspace_bytes is None:
-        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        workspace_bytes = held
+    elif workspace_bytes < 0 or isinstance(workspace, torch.Tensor) and workspace_bytes > held:
+        raise ValueError(f"gdn_ssm_scan: a workspace of {held} bytes, not {workspace_bytes}")
     return _call("gdn_ssm_scan", shape,
                  (cu_seqlens, xbc, dt, A_log, dt_bias, D, state, state_out, y, workspace),
                  (int(workspace_bytes),), stream, check)
