@@ -87,13 +87,13 @@ _TORCH = {GDN_F32: torch.float32, GDN_F16: torch.float16, GDN_BF16: torch.bfloat
 
 @functools.lru_cache(maxsize=256)
 def _plan(name: str, raw: bytes):
-    """(argument, type, elements, strides, size) of a call's tensors, from the bytes
+    """(argument, type, elements, strides, rows) of a call's tensors, from the bytes
     of its shape.  strides None: a tensor without gaps, of that many elements."""
     def flat(arg, dtype, least):
         return arg, dtype, least, None, None
 
     def rows(arg, dtype, n, cols, stride):
-        return arg, dtype, None, (stride or cols, 1), (n, cols)
+        return arg, dtype, n * cols, (stride or cols, 1), n
 
     i32, f32 = torch.int32, torch.float32
     if name == "gdn_group_norm":
@@ -118,7 +118,7 @@ def _plan(name: str, raw: bytes):
     return (raw_x, w, b, dt, *heads, *hist, *state, y)
 
 
-def _refuse(name: str, x, arg, dtype, least, strides, size):
+def _refuse(name: str, x, arg, dtype, least, strides, n):
     """ValueError if `x` is not the tensor of this entry of the plan; _call comes
     here with what is not so at first sight."""
     if dtype is not None and x.dtype is not dtype:
@@ -129,7 +129,7 @@ def _refuse(name: str, x, arg, dtype, least, strides, size):
         if x.numel() < least:
             raise ValueError(f"{name}: {arg} has {x.numel()} elements of {least}")
         return
-    n, cols = size
+    cols = least // n if n > 0 else 0
     if x.is_contiguous():
         fits = n <= 0 or x.numel() >= (n - 1) * strides[0] + cols
     else:
@@ -155,13 +155,13 @@ def _call(name: str, shape, tensors, tail, stream, check: bool) -> int:
     """One library call: addresses, then `tail`, then the stream."""
     dev = -1
     args = []
-    for x, (arg, dtype, least, strides, size) in zip(tensors, _plan(name, bytes(shape))):
-        if x is None or isinstance(x, int):
+    for x, (arg, dtype, least, strides, n) in zip(tensors, _plan(name, bytes(shape))):
+        if x is None or type(x) is int:
             args.append(x)
             continue
         if x.dtype is not dtype or not (x.is_contiguous() and x.numel() >= least if strides is None
-                                        else x.shape == size and x.stride() == strides):
-            _refuse(name, x, arg, dtype, least, strides, size)
+                                        else x.stride() == strides and x.size(0) == n and x.numel() == least):
+            _refuse(name, x, arg, dtype, least, strides, n)
         at = x.get_device()
         if at != dev or at < 0:
             if at < 0:
