@@ -114,7 +114,7 @@ __device__ __forceinline__ float exp_neg(float x)
 }
 
 // log(1 + e) for 0 <= e <= 1 to about 3 ulp: 2 atanh(s), s = e / (2 + e) <= 1/3,
-// by its series; s^17 / 17 is below 2^-30 of the sum
+// by its series; what follows s^15 / 15 is below 2^-29 of the sum
 __device__ __forceinline__ float log1p_unit(float e)
 {
     const float d = 2.0f + e, q = __builtin_amdgcn_rcpf(d);

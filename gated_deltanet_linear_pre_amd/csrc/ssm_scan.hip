@@ -22,32 +22,32 @@
 // p); wave w owns rows 16w..16w+15 of them, S in its accumulators as [n][p]
 // tiles of 16 x 16 (N/4 registers a lane).  The tile rows are numbered so that
 // lane (g, p) holds n = 32j + 8g + 0..7, which is at once the operand layout
-// of S in S C^T: the state never moves.  B, C and x of a chunk lie in LDS,
-// padded by 16 bytes a row (16-byte column reads of 16 rows then touch every
-// bank once); x^T and B^T are read by the transposing LDS reads.  The waves
-// share M: wave w forms its t tile w and writes it to LDS as an operand.  The
-// next chunk's rows are loaded to registers while this one is computed.
+// of S in S C^T: the state never moves.  B, C and x of a chunk lie in LDS (their
+// pitches: ScanShared); x^T and B^T are read by the transposing LDS reads.  The
+// waves share M: each forms some of its 16 x 16 tiles (form_m's callers) and
+// writes them to LDS as operands.  The next chunk's rows are loaded to registers
+// while this one is computed.
 //
 // Precision.  bf16 (and fp16, fp32) inputs enter the products as they are.  The
 // fp32 operands (S, M and the weighted x) are split into parts of the matrix
 // type whose products are summed in fp32, whatever y's type:
-//   bf16: 3 parts, 24 bits.  (2 parts are off by up to 2^-17 of a term; where the
-//         terms cancel, y rounded to bf16 showed it: 0.2% of the outputs came out
-//         one step from those of an fp32 evaluation);
+//   bf16: 3 parts, 24 bits.  (2 parts are off by up to 2^-17 of a term, and 0.1% of
+//         the outputs of bf16 came out one step from those of an fp32 evaluation:
+//         1.0e-4 of y.  The third part costs 332 -> 411 us on the packed batch);
 //   fp16: 2 parts, off by at most 2^-23 of a value (an fp32 rounding: 2^-24) or
 //         2^-38 of the largest value of the row or column that shares a
 //         contraction, to which all are scaled by a power of two, as fp16's range
 //         asks.  That is below what the sums of an fp32 evaluation lose;
 //   fp32: one part, on the fp32 matrix instructions.
 //
-// Bound.  At 16 bits by what a wave can issue between the barriers of a chunk:
-// about 100 matrix instructions of 16 cycles and 550 vector ones a wave and chunk
-// of 64 tokens at N = 128, which take 9000 cycles with two blocks on a CU; the
-// matrix pipe is busy 27% of the time, HBM moves 1.7 TB/s.  fp32 is bound by the
-// rate of its matrix instructions, an eighth of the 16-bit one.  Measured, 64
-// heads of 64, N = 128: 2048 tokens bf16 45 us (end states 14, segments 8,
-// outputs 26), fp16 48, fp32 98; 27135 tokens in
-// 4 sequences bf16 331 us (end states 85).
+// Bound.  At 16 bits by what a wave can issue between the barriers of a chunk: with
+// three parts, N = 128, 57 matrix instructions of 16 cycles and 450 vector ones of 4
+// a wave and chunk of 32 tokens, 2700 cycles, of which three waves share a SIMD:
+// the 7800 cycles that a chunk of the packed batch takes.  The matrix pipe is busy
+// 23% of the time, HBM moves 1.4 TB/s.  fp32 is bound by the rate of its matrix
+// instructions, an eighth of the 16-bit one.  Measured, 64 heads of 64, N = 128:
+// 2048 tokens bf16 51 us (end states 15, segments 8, outputs 33), fp16 49 (14, 8,
+// 30), fp32 98 (31, 8, 67); 27135 tokens in 4 sequences bf16 417 us (end states 89).
 #include <type_traits>
 
 #include "ssm_device.h"
@@ -95,8 +95,9 @@ template <> struct Mat<float> {
 // Tokens of a chunk; PARTS: those of M in LDS.  64 halve the times that S is split into operands; 32 leave
 // LDS for two blocks on a CU with N = 256 or fp32, and for three with three
 // parts of S and M.  Measured: N = 256, bf16 to fp32, 2005 tokens of 32 heads of
-// 128: 92 us by 32, 101 by 64; N = 128, 2048 tokens of 64 heads of 64, bf16 to
-// fp32: 50 and 58; fp16 to fp16, 8192 tokens: 104 and 90.
+// 128: 80 us by 32, 104 by 64; N = 128, 64 heads of 64, bf16, 2048 tokens 51 and 60,
+// 27135 packed tokens 417 and 487 (but 512 tokens 24.4 and 24.0); fp16, 8192 tokens:
+// 107 and 93.
 template <typename T, int N, int PARTS> constexpr int chunk_tokens()
 {
     return sizeof(T) == 4 || N == 256 || (N == 128 && PARTS == 3) ? 32 : 64;
@@ -384,7 +385,7 @@ __device__ __forceinline__ bool locate(const SsmDims &d, const ScanArgsT &a, Par
     // blocks go to the 8 XCDs in turn: neighbouring heads, which share B and C,
     // go to one XCD and its L2; in another order for each segment, or a CU would
     // get two blocks of one head, which a slow decay makes long in the end states
-    // (packed batch 338 -> 331 us)
+    // (packed batch 425 -> 417 us)
     const unsigned each = gridDim.x / 8;
     const int bx = gridDim.x % 8 ? blockIdx.x : blockIdx.x % 8 * each + (blockIdx.x / 8 + (unsigned)b.slot) % each;
     b.h = bx / pt_n;
@@ -639,7 +640,7 @@ __global__ __launch_bounds__(256, N == 128 && Mat<TI>::PARTS == 3 ? 3 : 2) void 
             } else if constexpr (MT::scaled) {  // a row's scale is that of all its columns
                 if (mt == 0) form_m(i0, i0, i1, bt);
                 else if (mt == 1) form_m(i1, i0, i2, bt);
-            } else {  // a tile a wave (2048 tokens fp32 100 -> 98 us)
+            } else {  // a tile a wave (packed batch 423 -> 417 us)
                 if (w == 0) form_m(i0, i0, i1, bt);
                 else if (w == 1) form_m(i1, i0, i1, bt);
                 else if (w == 2) form_m(i1, i1, i2, bt);
@@ -728,8 +729,8 @@ __global__ __launch_bounds__(256, N == 128 && Mat<TI>::PARTS == 3 ? 3 : 2) void 
                 for (int k = 0; k < KK; ++k) split8<TI, PARTS>(u[k], uf[k]);
                 __builtin_amdgcn_sched_barrier(0);
                 // (in two parts of n, which bounds the registers: at N = 128 all
-                // of B^T at once spilled some, and 430 us on the packed batch
-                // of 27135 tokens became 490)
+                // of B^T at once takes 417 us on the packed batch of 27135 tokens
+                // to 481, and 79 of the ragged one at N = 256 to 125)
                 constexpr int JS = J < 2 ? J : J / 2;
 #pragma unroll
                 for (int j0 = 0; j0 < J; j0 += JS) {
@@ -1092,9 +1093,10 @@ constexpr int NO_SEGMENTS = 1 << 30;  // tokens: more than a call may have
 // blocks each, which hide one another's latency; where that would leave a block
 // 128 tokens or less, one block each, of at least 128.  A batch of sequences of
 // up to 256 tokens is not cut: two segments cost two more kernels' latency.
-// Measured, 64 heads of 64, N = 128, bf16, by blocks: 2048 tokens 256 50 us, 512
-// 45, 1024 44; 27135 packed tokens 530, 398, 420; 1024 tokens 256 31.6, 512
-// 34.7; 512 tokens 128 28.5, 256 22.6, 512 29; 256 tokens 64 17, 128 20.
+// Measured, 64 heads of 64, N = 128, bf16, by blocks: 2048 tokens 256 58.8 us, 512
+// 50.8, 1024 60.8; 27135 packed tokens 567, 417, 411; 1024 tokens 256 36, 512 38;
+// 512 tokens 128 34, 256 24.4, 512 34; 4 sequences of 256 uncut 24.8, 512 30.8; one
+// of 256 uncut 21.3, 128 22.5 (256 blocks of 64 tokens 18.9).
 int segment_tokens(const SsmDims &d, int64_t max_T)
 {
     const int64_t all = d.T * d.H * ((d.P + 63) / 64);  // tokens of all blocks
@@ -1109,8 +1111,9 @@ int segment_tokens(const SsmDims &d, int64_t max_T)
 // Up to this many segments of a sequence the chunk kernel's blocks run over the
 // ones before theirs themselves, which costs them reads that grow with the
 // segments and saves a launch.  Measured against ssm_segment_kernel, as above:
-// 2 segments 28.9 and 32.4 us, 4 31.7 and 35.6, 7 35.5 and 37.2, 8 49.0 and 47.7
-// (fp16), 16 122 and 111.
+// 4 segments 24.4 and 31.2 us (512 tokens), 35.9 and 40.6 (1024), 7 39.9 and 41.3
+// (1280), 48.1 and 48.4 (1792), 8 50.6 and 51.0 (2048), 16 143 and 133 (16384 of 32
+// heads).
 constexpr int JOIN_SEGMENTS = 7;
 
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
