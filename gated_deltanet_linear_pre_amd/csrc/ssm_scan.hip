@@ -92,12 +92,12 @@ template <> struct Mat<float> {
     }
 };
 
-// Tokens of a chunk; PARTS: those of M in LDS.  64 halve the times that S is split into operands; 32 leave
-// LDS for two blocks on a CU with N = 256 or fp32, and for three with three
-// parts of S and M.  Measured: N = 256, bf16 to fp32, 2005 tokens of 32 heads of
-// 128: 80 us by 32, 104 by 64; N = 128, 64 heads of 64, bf16, 2048 tokens 51 and 60,
-// 27135 packed tokens 417 and 487 (but 512 tokens 24.4 and 24.0); fp16, 8192 tokens:
-// 107 and 93.
+// Tokens of a chunk; PARTS: those of M in LDS.  64 halve the times that S is split
+// into operands; 32 leave LDS for two blocks on a CU with N = 256 or fp32, and for
+// three with three parts of S and M.  Measured: N = 256, bf16 to fp32, 2005 tokens of
+// 32 heads of 128: 80 us by 32, 104 by 64; N = 128, 64 heads of 64, bf16, 2048 tokens
+// 51 and 60, 27135 packed tokens 417 and 487 (but 512 tokens 24.4 and 24.0); fp16,
+// 8192 tokens: 107 and 93.
 template <typename T, int N, int PARTS> constexpr int chunk_tokens()
 {
     return sizeof(T) == 4 || N == 256 || (N == 128 && PARTS == 3) ? 32 : 64;
