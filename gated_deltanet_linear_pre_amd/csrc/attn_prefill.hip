@@ -108,8 +108,6 @@ hipError_t attend(const gdn_attn_shape &s, const AttnArgs &a, hipStream_t st)
 } // namespace
 
 size_t attn_prefill_workspace_bytes(const gdn_attn_shape &) { return 0; }
-size_t attn_step_workspace_bytes(const gdn_attn_shape &) { return 0; }
 hipError_t launch_attn_prefill(const gdn_attn_shape &s, const AttnArgs &a, hipStream_t st) { return attend(s, a, st); }
-hipError_t launch_attn_step(const gdn_attn_shape &s, const AttnArgs &a, hipStream_t st) { return attend(s, a, st); }
 
 } // namespace gdn
