@@ -42,7 +42,7 @@ int check_shape(const gdn_attn_shape *s)
     if (s->heads / s->kv_heads > kMaxGroup) return GDN_E_SHAPE;
     const int D = s->head_dim;
     if (D != 64 && D != 96 && D != 128 && D != 192 && D != 256) return GDN_E_SHAPE;
-    if (s->page_size < 8 || s->page_size > 1024 || (s->page_size & (s->page_size - 1))) return GDN_E_SHAPE;
+    if (s->page_size < 16 || s->page_size > 1024 || (s->page_size & (s->page_size - 1))) return GDN_E_SHAPE;
     if (s->n_seq < 1 || s->n_seq > kMaxSeqs) return GDN_E_SHAPE;
     if (s->total_T < 0 || s->total_T > kMaxRows) return GDN_E_SHAPE;
     if (s->max_T < 0 || s->max_T > s->total_T) return GDN_E_SHAPE;

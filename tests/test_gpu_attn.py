@@ -106,7 +106,7 @@ IO = ["f32", "f16", "bf16"]
 APPEND = [
     # new, past, H, KV, D, page, rope, pairs, norm
     ([1], [0], 1, 1, 64, 16, 64, False, False), ([1], [700], 16, 2, 256, 64, 64, False, True),
-    ([37], [0], 6, 2, 64, 16, 32, True, False), ([5, 0, 1, 90], [3, 9, 100, 0], 4, 4, 128, 8, 128, True, True),
+    ([37], [0], 6, 2, 64, 16, 32, True, False), ([5, 0, 1, 90], [3, 9, 100, 0], 4, 4, 128, 16, 128, True, True),
     ([30, 2], [0, 1], 3, 1, 96, 32, 48, False, True), ([17, 16, 15], [15, 16, 17], 8, 2, 192, 16, 192, True, False),
     ([300], [1], 2, 1, 256, 1024, 0, False, True), ([3], [40], 2, 2, 96, 16, 16, True, True),
     ([2000], [5], 2, 1, 64, 128, 48, False, True), ([9000, 300], [0, 0], 1, 1, 64, 64, 64, False, False),
@@ -170,11 +170,11 @@ def test_append_at_far_and_given_positions(gpu, io):
 
 def test_append_leaves_out_what_has_no_place(gpu):
     # more new tokens than the cache holds: the first three stand below 0; the last two not below max_kv
-    c = Case([8, 2], [-3, 4], 2, 1, 64, 8, "bf16")
+    c = Case([20, 2], [-3, 4], 2, 1, 64, 16, "bf16")
     banner("gdn_attn_append negative positions")
     check_append(c, 32, False, True, 4)
-    c = Case([8], [10], 2, 1, 64, 8, "f32")
-    c.table_t[0, 1] = -1  # a page of none: rows 8..15
+    c = Case([16], [20], 2, 1, 64, 16, "f32")
+    c.table_t[0, 1] = -1  # a page of none: positions 16..31
     was = c.pages.t.clone()
     rng = np.random.default_rng(5)
     proj, q, k, v, w, freq = append_inputs(c, 32, True, rng)
@@ -183,16 +183,16 @@ def test_append_leaves_out_what_has_no_place(gpu):
     q_out = torch.empty(c.T, c.H * c.D, device="cuda")
     attn.gdn_attn_append(s, c.cu_t, c.kv_t, c.table_t, None, q, k, v, freq, *w, q_out, c.k, c.v)
     torch.cuda.synchronize()
-    rows = torch.zeros(c.n_pages, 8, dtype=torch.bool, device="cuda")
-    rows[int(c.table[0, 2]), :2] = True  # positions 16 and 17
+    rows = torch.zeros(c.n_pages, 16, dtype=torch.bool, device="cuda")
+    rows[int(c.table[0, 2]), :4] = True  # positions 32 to 35
     assert torch.equal(was.transpose(1, 3)[~rows], c.pages.t.transpose(1, 3)[~rows])
-    assert torch.equal(c.v[int(c.table[0, 2]), 0, :2], v[6:8])
+    assert torch.equal(c.v[int(c.table[0, 2]), 0, :4], v[12:16])
 
 
 # ------------------------------------------------------------------- attention
 PREFILL = [
     # new, past, H, KV, D, page
-    ([1], [0], 1, 1, 64, 16), ([37], [0], 6, 2, 64, 16), ([1, 0, 2, 31, 32, 33], [0, 5, 63, 1, 0, 31], 4, 2, 128, 8),
+    ([1], [0], 1, 1, 64, 16), ([37], [0], 6, 2, 64, 16), ([1, 0, 2, 31, 32, 33], [0, 5, 63, 1, 0, 31], 4, 2, 128, 16),
     ([64, 65, 63], [0, 0, 64], 8, 8, 96, 16), ([130, 5], [70, 500], 16, 2, 256, 64), ([40], [25], 5, 1, 192, 32),
     ([300], [0], 2, 1, 128, 1024), ([3, 2], [0, 90], 128, 1, 64, 16), ([17], [1000], 12, 4, 64, 16), ([2], [2000], 3, 3, 128, 16),
 ]
@@ -216,7 +216,7 @@ def test_prefill_window(gpu, io, window):
 STEP = [
     # kv lengths, H, KV, D, page
     ([1], 1, 1, 64, 16), ([1, 2, 15, 16, 17, 31, 32, 33], 16, 2, 128, 16), ([127, 128, 129, 0, 255, 256, 257], 8, 1, 256, 64),
-    ([700], 16, 2, 256, 64), ([3000, 1, 0, 511], 8, 8, 64, 8), ([100, 1000], 128, 1, 96, 32), ([65, 300], 34, 2, 192, 16),
+    ([700], 16, 2, 256, 64), ([3000, 1, 0, 511], 8, 8, 64, 16), ([100, 1000], 128, 1, 96, 32), ([65, 300], 34, 2, 192, 16),
     ([9000], 32, 8, 128, 16), (list(range(0, 200, 7)), 6, 3, 64, 16),
 ]
 
@@ -334,7 +334,7 @@ def test_sequence_bounds_outside_the_rows(gpu):
 
 # ------------------------------------------------------------------------ copy
 @pytest.mark.parametrize("io", IO)
-@pytest.mark.parametrize("KV,D,page,n", [(1, 64, 8, 1), (2, 256, 64, 3), (3, 96, 16, 40), (8, 128, 16, 200)])
+@pytest.mark.parametrize("KV,D,page,n", [(1, 64, 16, 1), (2, 256, 64, 3), (3, 96, 16, 40), (8, 128, 16, 200)])
 def test_copy_pages(gpu, io, KV, D, page, n):
     rng = np.random.default_rng([13, n])
     N = 2 * n + 5
