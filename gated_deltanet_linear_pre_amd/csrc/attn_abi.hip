@@ -13,7 +13,7 @@ using gdn::AttnArgs;
 constexpr int kMaxHeads = 1 << 12;
 constexpr int kMaxGroup = 128;
 constexpr int kMaxSeqs = 1 << 16;
-constexpr int64_t kMaxRows = (int64_t)1 << 27;
+constexpr int64_t kMaxRows = (int64_t)1 << 26;  // (8 rows a block of 256 threads: a launch has less than 2^32 of them)
 constexpr int64_t kMaxKv = (int64_t)1 << 30;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 constexpr int64_t kMaxCache = (int64_t)1 << 56;  // elements

@@ -4,33 +4,41 @@
 //   o = sum_j w_j V_j / sum_j w_j,  w_j = exp(scale q.K_j - max)   over the keys a token sees
 //
 // One pass over the keys with the running maximum and sum of the softmax.  The g
-// query heads of a key-value head share its keys: a block's 128 rows are g heads of
-// 128 / g consecutive tokens, whatever g is, so a short prompt fills its rows too.
-// Bound by the matrix pipes and, beside them, by the vector unit's exponentials.
+// query heads of a key-value head share its keys: a block's rows (128; 64 for fp32) are g heads
+// of as many consecutive tokens as fit, whatever g is, so a short prompt fills its rows
+// too.  Bound by what a wave can issue between its products: matrix instructions, their
+// LDS reads and the softmax.
 //
-// gfx950 mapping.  Wave w of 4 takes rows 32w..32w+31 as the columns of 32 x 32
-// matrix products.  S^T = K Q^T puts a key a row and a query a column: maximum and
-// sum of a query stay in its two lanes, and the weights of lane (h, c) are keys
-// 4 h + 0..3 of every 8, which is at once the operand of O^T = V^T w if V^T is read
-// in the same order of keys.  So neither the weights nor O move between lanes.
-// Tiles of KT keys go from memory through registers to LDS, one tile ahead and in two
-// buffers, one barrier a tile; V^T is read by the transposing LDS reads.
+// gfx950 mapping.  A wave takes W rows (32; 16 where a head is wide) as the columns of
+// W x W matrix products.  S^T = K Q^T puts a key a row and a query a column: maximum and sum of a
+// query stay in its lanes, and the weights of lane (h, c) are 4 consecutive keys of
+// every 4 G, which is at once the operand of O^T = V^T w if V^T is read in the same order
+// of keys.  So neither the weights nor O move between lanes.  Tiles of KT keys go from memory to LDS
+// directly, one tile ahead, in two buffers, one barrier a tile, their copies spread over the
+// products; V^T is read by the transposing LDS reads.  8 waves share a tile at D = 256, where
+// 4 would spend 40% of the time on the copies (through registers: 8192 tokens of 16 heads 0.77 ms,
+// copied by 4 waves 0.69, by 8 0.67, spread 0.64).
 //
 // The maximum that the weights are taken against follows the scores only when they
 // pass it by 2^8: O and the sum are scaled then, at most a few times a row, and
 // weights up to 2^8 lose nothing.
 //
-// Few rows over many keys (a chunk that goes on from a long cache) would leave most
-// CUs idle: the keys are then cut in pieces, a block each, whose sums, maxima and O a
-// second kernel joins.
+// Few rows over many keys (a chunk that goes on from a long cache) would leave most CUs idle.
+// The keys of all rows then form one line that is cut into equal parts, one a block, as in the
+// step: rows within one part are finished there, of rows that are cut each part leaves O, maximum
+// and sum in the workspace, and a second kernel joins them.
 //
 // Precision.  Scores, maxima, sums and O are fp32; 16-bit weights are rounded to the
 // io type for the product with V (half a step of each weight, of random sign: as much as
 // the rounding of the output; a second part would be half of the products again).
 //
 // In a tile that a row does not see whole hidden scores are -inf, their weights 0.  A
-// V that is not finite would turn 0 into NaN there, so it goes to LDS as 0 in such
-// a tile, and the rows that see it are made NaN in its channel.
+// V that is not finite would turn 0 into NaN there, so it is made 0 in LDS in such
+// a tile, and the rows that see it become NaN in its channel at the end.
+//
+// Measured: 2048 tokens of 32 heads of 128, fp16, 53 us (650 TFLOP/s of what the mask leaves), 8192
+// tokens 0.60 ms (912); 8192 tokens of 16 heads of 256, bf16, 0.62 ms (882); chunks of
+// 391 tokens over caches of up to 32768 keys 223 us (712).
 #include "attn_device.h"
 #include "mfma_device.h"
 
@@ -38,7 +46,6 @@ namespace gdn {
 
 namespace {
 
-constexpr int BLOCK = 256;
 typedef float f16v __attribute__((ext_vector_type(16)));
 
 // Products of W x W values over 8 G deep operands, G = 64 / W lane groups: lane (h, c)
@@ -87,60 +94,76 @@ template <> struct Mma<float, 32> {
     }
 };
 
-#ifndef W_WIDE
-#define W_WIDE 16
-#endif
-#ifndef KT_NARROW
-#define KT_NARROW 64
-#endif
-#ifndef KT_WIDE
-#define KT_WIDE 32
-#endif
 template <typename T, int D> struct Tile {
-    static constexpr int W = sizeof(T) == 4 ? 16 : D <= 128 ? 32 : W_WIDE;  // rows of a wave
-    static constexpr int G = 64 / W, NA = W * W / 64, ROWS = 4 * W;
-    static constexpr int KT = sizeof(T) == 4 ? 32 : D <= 128 ? KT_NARROW : KT_WIDE;  // keys
+    static constexpr int W = sizeof(T) == 4 || D > 128 ? 16 : 32;  // rows of a wave
+    // Waves that share a tile, and blocks on a CU: 8 waves of 256 registers; fp32 of wide heads, whose queries alone
+    // take up to 64, 4 of 512
+    static constexpr bool big = sizeof(T) == 4 && D > 128;
+    static constexpr int WAVES = D > 128 && !big ? 8 : 4, BLOCK = 64 * WAVES, BLOCKS = D > 128 ? 1 : 2;
+    static constexpr int G = 64 / W, NA = W * W / 64, ROWS = WAVES * W;
+    static constexpr int KT = sizeof(T) == 4 || D == 256 ? 32 : 64;  // keys
     static constexpr int NT = KT / W, NC = D / (8 * G), ND = D / W, NK = KT / (8 * G);
     // operands read from LDS ahead of their product.  Their registers are those of a product whose
     // result the product just issued took as its sum: no load is given registers of an operand in use.
-    static constexpr int AHEAD = 4;
-    static constexpr int V = Vec16<T>::n;
-    static constexpr int NV = KT * D / V / BLOCK;  // vectors of K (and of V) a thread moves
-    static constexpr int E16 = 16 / sizeof(T);
-    static constexpr int KP = D + (W == 32 ? 1 : 2) * E16;  // pitch of K's rows in LDS
-    // of V's rows.  16 bits: a transposing read takes 2 W bytes of 4 rows a lane group: an odd multiple of 2 W.
-    // fp32: 32 bytes more
-    static constexpr int VP = sizeof(T) == 4 ? D + 8 : D / W % 2 ? D : D + W;
-    static constexpr int BLOCKS = D <= 128 || (W == 16 && sizeof(T) == 2) ? 2 : 1;  // on a CU
-    static_assert(NV * BLOCK * V == KT * D, "whole vectors");
+    static constexpr int AHEAD = sizeof(T) == 4 ? 2 : D == 96 ? 3 : 4;
+    static constexpr int V = Vec16<T>::n, LINE = D / V;  // values of a vector of 16 bytes, vectors of a row
+    static constexpr int NV = KT * LINE / BLOCK;         // vectors of K (and of V) a thread moves
+    static_assert(NV * BLOCK == KT * LINE, "whole vectors");
+    static_assert(16 * LINE % 64 == 0, "16 rows are whole vectors of a wave");
+
+    // Rows lie in LDS without gaps; vector x of a row stands at place x ^ swap of its row, which lets a read
+    // meet every bank once.  FOLD: rows (of 4 banks a vector, 64 in all) until the banks repeat.
+    static constexpr int FOLD = LINE % 16 == 0 ? 1 : LINE % 8 == 0 ? 2 : 4;
+    // K: 16 rows of one vector
+    static __device__ __forceinline__ int swap_k(int row) { return (row / FOLD) & (16 / FOLD - 1); }
+    // V: 16 bits, 2 W bytes (UNIT vectors) of 16 / UNIT rows; fp32, 4 vectors of rows that are 4 apart
+    static constexpr int UNIT = sizeof(T) == 4 ? 4 : W / 8, APART = sizeof(T) == 4 ? 4 : 1;
+    static constexpr int SHIFT = FOLD > APART ? FOLD : APART, KINDS = 16 / UNIT / FOLD > 0 ? 16 / UNIT / FOLD : 1;
+    static __device__ __forceinline__ int swap_v(int row) { return (row / SHIFT) % KINDS * UNIT; }
+    static_assert(LINE % (16 / FOLD) == 0 && LINE % (KINDS * UNIT) == 0, "vectors change places within a row");
 };
 
 struct PrefillArgs {
     AttnArgs a;
     int heads, parts;  // of a key-value head's group that a block takes; parts of the group
-    int tokens;   // of a block: rows / heads
-    int slots;    // blocks along the tokens
-    int pieces;   // of a row's keys, at most
-    int piece;    // keys of a piece
-    float2 *ml;   // [slot][KV parts][pieces][rows]
-    float *o;     // [slot][KV parts][pieces][rows][D]
+    int tokens;        // of a block: rows / heads
+    int slots;         // blocks along the tokens
+    int line;          // blocks among which all keys are dealt in equal parts; 0: a block takes its rows' keys
+    // of the line's parts
+    struct Place *place;  // [line]
+    float2 *ml;           // [2 line][rows] maximum (of scores times scale log2 e) and sum of weights
+    f4 *o;                // [2 line][wave][4 channels of a row, as a lane holds them][lane]
 };
 
-// out = o r, gated, 4 channels
-template <typename T>
-__device__ __forceinline__ void finish(const AttnDims &d, const AttnArgs &a, int64_t row, int head, int col, f4 o, float r)
-{
+// Keys that rows are cut at, and the longest line of slots
+constexpr int CHUNK = 128, MOST_SLOTS = 512;
+
+// Where a part of the line begins: rows (-1: the part is empty), their heads, chunk of theirs and
+// chunks in all, chunks of a part
+struct Place {
+    int slot, hy, ch, nc;
+    unsigned quantum;
+};
+
+__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// 4 channels of an output row: its gate's values, and o r, gated
+template <typename T> struct Quad {
     typedef T t4 __attribute__((ext_vector_type(4)));
-    t4 y;
-    if (a.gate) {
-        const t4 gate = *reinterpret_cast<const t4 *>(static_cast<const T *>(a.gate) + row * d.gate_stride + head * d.D + col);
+};
+template <typename T>
+__device__ __forceinline__ typename Quad<T>::t4 gate_of(const AttnDims &d, const AttnArgs &a, int64_t row, int head, int col)
+{
+    return *reinterpret_cast<const typename Quad<T>::t4 *>(static_cast<const T *>(a.gate) + row * d.gate_stride + head * d.D + col);
+}
+template <typename T>
+__device__ __forceinline__ void finish(const AttnDims &d, const AttnArgs &a, int64_t row, int head, int col, f4 o, float r,
+                                       typename Quad<T>::t4 gate)
+{
+    typename Quad<T>::t4 y;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = (T)(o[i] * r / (1.0f + expf(-(float)gate[i])));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = (T)(o[i] * r);
-    }
-    *reinterpret_cast<t4 *>(static_cast<T *>(a.out) + (row * d.H + head) * d.D + col) = y;
+    for (int i = 0; i < 4; ++i) y[i] = (T)(a.gate ? o[i] * r * __builtin_amdgcn_rcpf(1.0f + exp_fast(-(float)gate[i])) : o[i] * r);
+    *reinterpret_cast<typename Quad<T>::t4 *>(static_cast<T *>(a.out) + (row * d.H + head) * d.D + col) = y;
 }
 // 1 / sum of weights; no key: o and the sum are 0 (a NaN stays one)
 __device__ __forceinline__ float inverse_sum(float l) { return l > 0.f ? 1.0f / l : l; }
@@ -169,10 +192,17 @@ struct Work {
     int begin, end;       // keys that the rows see (begin: on a tile)
 };
 template <int KT>
-__device__ __forceinline__ bool locate(const AttnDims &d, const PrefillArgs &s, int slot, Work &b)
+__device__ __forceinline__ bool locate(const AttnDims &d, const PrefillArgs &s, int slot, Work &b, int seq = -1)
 {
     SeqTile st;
-    if (!find_tile(s.a.cu, d.n_seq, d.T, s.tokens, slot, st)) return false;
+    if (seq >= 0) {  // known
+        st.n = seq;
+        st.begin = seq_bound(s.a.cu, seq, d.T);
+        st.end = seq_bound(s.a.cu, seq + 1, d.T);
+        st.c = slot - (st.begin / s.tokens + seq);
+    } else if (!find_tile(s.a.cu, d.n_seq, d.T, s.tokens, slot, st)) {
+        return false;
+    }
     const int len = st.end - st.begin, first = st.c * s.tokens;
     if (first >= len) return false;
     b.n = st.n;
@@ -186,28 +216,47 @@ __device__ __forceinline__ bool locate(const AttnDims &d, const PrefillArgs &s, 
 }
 
 // V^T: channel W t + c, keys 8 G k + 4 h + 0..3 and 4 G more
-template <typename T, int W, int VP>
+template <typename T, int D>
 __device__ __forceinline__ typename Mat<T>::frag column(const T *v, int k, int t, int lane)
 {
-    constexpr int G = 64 / W;
+    typedef Tile<T, D> TL;
+    constexpr int G = TL::G, W = TL::W, V = TL::V;
     if constexpr (sizeof(T) == 4) {
-        const T *p = v + (8 * G * k + 4 * (lane / W)) * VP + W * t + (lane & (W - 1));
+        // (the rows 8 G k.. are whole periods of the places, and the four rows of a lane share theirs)
+        static_assert(TL::SHIFT >= 4 && 4 * G % (TL::SHIFT * TL::KINDS) == 0, "one address for all rows");
         typename Mat<T>::frag f;
+        const int row = 4 * (lane / W), ch = W * t + (lane & (W - 1));
+        const T *p = v + (8 * G * k + row) * D + ((ch / V) ^ TL::swap_v(row)) * V + ch % V;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[i] = p[i * VP];
-            f[i + 4] = p[(i + 4 * G) * VP];
-        }
+        for (int i = 0; i < 8; ++i) f[i] = p[((i & 3) + (i >> 2) * 4 * G) * D];
         return f;
     } else {
         typedef short s4 __attribute__((ext_vector_type(4)));
         typedef short s8 __attribute__((ext_vector_type(8)));
         typedef __attribute__((address_space(3))) s4 lds_s4;
-        const T *p = v + (8 * G * k + 4 * (lane / W) + ((lane & 15) >> 2)) * VP + W * t + 16 * ((lane >> 4) & (W / 16 - 1)) + 4 * (lane & 3);
+        // (the second read's row is 4 G further, which changes no vector's place)
+        static_assert(4 * G % (TL::SHIFT * TL::KINDS) == 0, "one address for both reads");
+        const int row = 4 * (lane / W) + ((lane & 15) >> 2), ch = W * t + 16 * ((lane >> 4) & (W / 16 - 1)) + 4 * (lane & 3);
+        const T *p = v + (8 * G * k + row) * D + ((ch / V) ^ TL::swap_v(row)) * V + ch % V;
         const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(p));
-        const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(p + 4 * G * VP));
+        const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(p + 4 * G * D));
         return __builtin_bit_cast(typename Mat<T>::frag, (s8)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     }
+}
+
+// 16 bytes a lane from memory (base and the lane's offset) to LDS (`to`, lane after lane).  Written in
+// assembly because the compiler does not count it then: it would put a wait for all of them before
+// the next LDS read.  wait_vmem_all() and a barrier stand before the data is read.
+__device__ __forceinline__ void copy_to_lds(const void *base, unsigned offset, unsigned to)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // (that nobody saves m0 for us: nothing here keeps it)
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(to)),
+                     "v"(offset), "s"(base)
+                     : "memory", "m0");
+#pragma clang diagnostic pop
+#endif
 }
 
 // Keeps an operand's registers from being given away before this point
@@ -229,8 +278,8 @@ __device__ __forceinline__ void operand_in_use(const typename Mat<T>::frag &f)
 template <typename T>
 __device__ __forceinline__ bool not_finite(T x) { return !(fabsf((float)x) <= 3.402823466e38f); }
 
-template <typename T, int D>
-__global__ __launch_bounds__(BLOCK, (Tile<T, D>::BLOCKS)) void prefill_kernel(AttnDims d, PrefillArgs s)
+template <typename T, int D, bool LINED>
+__global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void prefill_kernel(AttnDims d, PrefillArgs s)
 {
     typedef Tile<T, D> TL;
     typedef typename Mat<T>::frag frag;
@@ -238,310 +287,447 @@ __global__ __launch_bounds__(BLOCK, (Tile<T, D>::BLOCKS)) void prefill_kernel(At
     typedef Mma<T, TL::W> MM;
     typedef typename MM::acc acc;
     constexpr int W = TL::W, G = TL::G, NA = TL::NA, UNITS = NA / 4;
+    constexpr int BLOCK = TL::BLOCK, LINE = TL::LINE;
     constexpr int KT = TL::KT, NT = TL::NT, NC = TL::NC, ND = TL::ND, NK = TL::NK, NV = TL::NV, V = TL::V;
-    __shared__ __attribute__((aligned(16))) T sk[2][KT * TL::KP];
-    __shared__ __attribute__((aligned(16))) T sv[2][KT * TL::VP];
+    __shared__ __attribute__((aligned(1024))) T sk[2][KT * D];
+    __shared__ __attribute__((aligned(1024))) T sv[2][KT * D];
     // of a tile that some row does not see whole: values of V that are not finite (0 in sv), a bit each,
     // and whether a wave met one
-    __shared__ unsigned char s_bits[2][KT * D / V];
-    __shared__ int s_bad[2][BLOCK / 64];
-    const int tid = threadIdx.x, lane = tid & 63, h = lane / W, c = lane & (W - 1);
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int slot = s.slots - 1 - blockIdx.x;  // (the rows with the most keys first)
-    const int kh = blockIdx.y / s.parts, head0 = kh * d.g + (blockIdx.y - kh * s.parts) * s.heads;
-    const int g = (kh + 1) * d.g - head0 < s.heads ? (kh + 1) * d.g - head0 : s.heads;
+    __shared__ unsigned char s_bits[2][KT * LINE];
+    __shared__ int s_bad[2][TL::WAVES];
+    const int w = scalar(threadIdx.x >> 6);
+    const int heads = d.KV * s.parts;
 
-    Work b;
-    if (!locate<KT>(d, s, slot, b)) return;
-    const int begin = b.begin + blockIdx.z * s.piece;
-    if (blockIdx.z > 0 && begin >= b.end) return;
-    const int end = b.end - begin > s.piece ? begin + s.piece : b.end;
-    const bool whole = blockIdx.z == 0 && end == b.end;
-
-    // ---- this lane's query: column c of the products ----
-    const int r = W * w + c;
-    const int used = b.tokens * g;
-    const int rr = r < used ? r : used - 1;  // (rows that are not there follow the last one, and are not written)
-    const int tok = rr / g, head = head0 + rr - tok * g;
-    const int p = b.p0 + tok, low = first_key(d, p);
-    // of the wave: the rows' first and last positions
-    const int wr = W * w < used ? W * w : used - 1, wl = W * w + W - 1 < used ? W * w + W - 1 : used - 1;
-    const int pw0 = b.p0 + wr / g, pw1 = b.p0 + wl / g;
-    const bool busy = W * w < used;
-    const int low_last = first_key(d, b.p0 + b.tokens - 1);
-    frag qf[NC];
-    {
-        const T *q = static_cast<const T *>(s.a.q) + (b.row + tok) * d.q_stride + (int64_t)head * D + 8 * h;
+    // ---- this block's rows, or its part of the line ----
+    __shared__ unsigned s_pre[LINED ? MOST_SLOTS + 1 : 1], s_sum[TL::WAVES];
+    __shared__ unsigned short s_seq[LINED ? MOST_SLOTS : 1];  // (less than 2^32 chunks: 512 rows of at most 2^23)
+    int slot = 0, hy = 0;
+    unsigned pos = 0, stop = 1, quantum = 0;
+    if constexpr (LINED) {
+        const int tid = threadIdx.x, lane = tid & 63;
+        const int per = (s.slots + BLOCK - 1) / BLOCK;
+        unsigned mine = 0;
+        for (int i = tid * per; i < s.slots && i < (tid + 1) * per; ++i) {
+            Work b;
+            const bool in = locate<KT>(d, s, i, b);
+            s_pre[i] = !in ? 0 : b.end - b.begin <= CHUNK ? 1 : (b.end - b.begin + CHUNK - 1) / CHUNK;
+            s_seq[i] = in ? b.n : 0;
+            mine += s_pre[i];
+        }
+        unsigned upto = mine;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) qf[i] = *reinterpret_cast<const typename Frag16<T>::type *>(q + 8 * G * i);
+        for (int u = 1; u < 64; u <<= 1) {
+            const unsigned x = __shfl_up(upto, u, 64);
+            if (lane >= u) upto += x;
+        }
+        if (lane == 63) s_sum[w] = upto;
+        __syncthreads();
+        unsigned total = 0;
+#pragma unroll
+        for (int i = 0; i < TL::WAVES; ++i) {
+            if (i < w) upto += s_sum[i];
+            total += s_sum[i];
+        }
+        unsigned at = upto - mine;
+        for (int i = tid * per; i < s.slots && i < (tid + 1) * per; ++i) {
+            const unsigned n = s_pre[i];
+            s_pre[i] = at;
+            at += n;
+        }
+        if (tid == 0) s_pre[s.slots] = total;
+        __syncthreads();
+        total = __builtin_amdgcn_readfirstlane(total * heads);
+        quantum = scalar(total / gridDim.x + (total % gridDim.x != 0));
+        const uint64_t from = (uint64_t)blockIdx.x * quantum;
+        pos = from < total ? (unsigned)from : total;
+        stop = total - pos < quantum ? total : pos + quantum;
+        if (pos == stop && threadIdx.x == 0) s.place[blockIdx.x].slot = -1;
+    } else {
+        // the rows with the most keys first; where all blocks are resident at once, those of the second round the
+        // other way about, so that a CU gets a long and a short one (2048 tokens 71 -> 59 us)
+        int q = blockIdx.z * gridDim.y + blockIdx.y;
+        if (q >= s.slots) return;
+        hy = blockIdx.x;
+        constexpr int FIRST = 256;
+        if (TL::BLOCKS == 2 && (int64_t)s.slots * heads <= 640) {
+            const int all = s.slots * heads, at = q * heads + hy;
+            if (at >= FIRST) {
+                q = scalar((all - 1 - (at - FIRST)) / heads);
+                hy = all - 1 - (at - FIRST) - q * heads;
+            }
+        }
+        slot = s.slots - 1 - q;
     }
-    acc o[ND];
-#pragma unroll
-    for (int t = 0; t < ND; ++t) o[t] = acc(0.f);
-    float m = -INFINITY, l = 0.f;
-    unsigned dead[(ND * NA + 31) / 32] = {};  // values of o that a V that is not finite has reached
-    const float cs = d.scale * 1.44269504f;
 
-    auto cut = [&](int k0) { return k0 + KT - 1 > b.p0 || k0 < low_last; };  // a row may not see all of a tile
+    while (pos < stop) {
+        int tid = threadIdx.x;
+#ifdef __HIP_DEVICE_COMPILE__
+        if (LINED) __asm__("" : "+v"(tid));  // (what is derived from it would be kept through the tiles for the next rows)
+#endif
+        const int lane = tid & 63, h = lane / W, c = lane & (W - 1);
+        bool whole = true;
+        int ch = 0, count = 0;
+        Work b;
+        if constexpr (LINED) {
+            int lo = 0, hi = s.slots;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if ((unsigned)scalar(s_pre[mid]) * heads <= pos) lo = mid;
+                else hi = mid;
+            }
+            slot = lo;
+            const unsigned here = scalar(s_pre[lo]), nc = scalar(s_pre[lo + 1]) - here;
+            const unsigned local = pos - here * heads, left = stop - pos;
+            hy = scalar(local / nc);
+            ch = local - hy * nc;
+            count = left < nc - ch ? left : nc - ch;
+            whole = count == (int)nc;
+            if (pos == blockIdx.x * quantum && tid == 0) s.place[blockIdx.x] = Place{slot, hy, ch, (int)nc, quantum};
+        }
+        const int kh = scalar(hy / s.parts), head0 = kh * d.g + (hy - kh * s.parts) * s.heads;
+        const int g = (kh + 1) * d.g - head0 < s.heads ? (kh + 1) * d.g - head0 : s.heads;
+        if (!locate<KT>(d, s, slot, b, LINED ? scalar(s_seq[slot]) : -1)) return;
+        // (the same for all lanes, which a compiler that divides in vector registers does not see)
+        b.n = scalar(b.n);
+        b.tokens = scalar(b.tokens);
+        b.row = scalar((int)b.row);
+        b.p0 = scalar(b.p0);
+        const int begin = scalar(b.begin) + ch * CHUNK, rows_end = scalar(b.end);
+        const int end = LINED && rows_end - begin > count * CHUNK ? begin + count * CHUNK : rows_end;
 
-    // ---- tiles from memory ----
-    const int32_t *table = s.a.table + (int64_t)b.n * d.table_pages;
-    // Vector i of a wave's 64 lanes lies in 16 consecutive rows (whole lines of D / V vectors
-    // never straddle 16 rows there), so in one page: its number and base are scalars.
-    const int64_t head_at = (int64_t)kh * d.page * D;
-    const T *K = static_cast<const T *>(s.a.k_cache) + head_at, *Vc = static_cast<const T *>(s.a.v_cache) + head_at;
-    vec rk[NV], rv[NV];
-    int page[NV];
-    constexpr int LINE = D / V;
-    static_assert(16 * LINE % 64 == 0, "16 rows are whole vectors of a wave");
-    constexpr bool even = BLOCK % LINE == 0;  // the same channel for every i
-    const int row0 = tid / LINE, col0 = (tid - row0 * LINE) * V;
-    auto row_of = [&](int i) { return even ? row0 + i * (BLOCK / LINE) : (i * BLOCK + tid) / LINE; };
-    auto col_of = [&](int i) { return even ? col0 : (i * BLOCK + tid - row_of(i) * LINE) * V; };
-    const int last = end - 1;
-    auto ask = [&](int k0) {  // the pages of a tile (behind the end: of the last key)
+        // ---- this lane's query: column c of the products ----
+        const int r = W * w + c;
+        const int used = b.tokens * g;
+        const int rr = r < used ? r : used - 1;  // (rows that are not there follow the last one, and are not written)
+        const int tok = rr / g, head = head0 + rr - tok * g;
+        const int p = b.p0 + tok, low = first_key(d, p);
+        // of the wave: the rows' first and last positions
+        const int wr = W * w < used ? W * w : used - 1, wl = W * w + W - 1 < used ? W * w + W - 1 : used - 1;
+        const int pw0 = b.p0 + scalar(wr / g), pw1 = b.p0 + scalar(wl / g);
+        const bool busy = W * w < used;
+        const int low_last = first_key(d, b.p0 + b.tokens - 1);
+        frag qf[NC];
+        {
+            const T *q = static_cast<const T *>(s.a.q) + (b.row + tok) * d.q_stride + (int64_t)head * D + 8 * h;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int key = k0 + (i * BLOCK + w * 64) / LINE;
-            page[i] = table[(unsigned)(key < end ? key : last) >> d.log_page];
+            for (int i = 0; i < NC; ++i) qf[i] = *reinterpret_cast<const typename Frag16<T>::type *>(q + 8 * G * i);
         }
-    };
-    auto load = [&](int k0) {
+        acc o[ND];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int64_t at = page_bound(d, __builtin_amdgcn_readfirstlane(page[i])) * d.page_stride;
-            int key = k0 + row_of(i);
-            key = key < end ? key : last;
-            const unsigned in = (unsigned)(key & (d.page - 1)) * D + col_of(i);
-            rk[i] = ld16_at(K + at, in * (unsigned)sizeof(T));
-            rv[i] = ld16_at(Vc + at, in * (unsigned)sizeof(T));
-        }
-    };
-    auto store = [&](int k0, int buf) {
-        if (cut(k0)) {
-            const bool tail = k0 + KT > end;
+        for (int t = 0; t < ND; ++t) o[t] = acc(0.f);
+        float m = -INFINITY, l = 0.f;
+        unsigned dead[(ND * NA + 31) / 32] = {};  // values of o that a V that is not finite has reached
+        const float cs = d.scale * 1.44269504f;
+
+        auto cut = [&](int k0) { return k0 + KT - 1 > b.p0 || k0 < low_last; };  // a row may not see all of a tile
+
+        // ---- tiles from memory ----
+        const int32_t *table = s.a.table + (int64_t)b.n * d.table_pages;
+        // Vector i of a wave's 64 lanes lies in 16 consecutive rows, so in one page: its number and first row are
+        // scalars.
+        const int64_t head_at = (int64_t)kh * d.page * D;
+        const T *K = static_cast<const T *>(s.a.k_cache) + head_at, *Vc = static_cast<const T *>(s.a.v_cache) + head_at;
+        auto top_of = [&](int i) { return (i * BLOCK + w * 64) / LINE; };  // the vector's first row
+        auto row_of = [&](int i) { return (i * BLOCK + tid) / LINE; };
+        auto from_of = [&](int i, int swap) {  // the lane's bytes from there, for its place in LDS
+            return (unsigned)(((row_of(i) - top_of(i)) * D + ((i * BLOCK + tid) % LINE ^ swap) * V) * sizeof(T));
+        };
+        const unsigned lds_k = (unsigned)(uintptr_t)(__attribute__((address_space(3))) void *)sk;
+        const unsigned lds_v = (unsigned)(uintptr_t)(__attribute__((address_space(3))) void *)sv;
+        const int last = end - 1;
+        // Lane i < NV (and NV + i) keeps the address of the wave's vector i of K (of V): a wave has a handful of them
+        static_assert(2 * NV <= 64, "a lane an address");
+        const int mine_top = (lane % NV * BLOCK + w * 64) / LINE;
+        const T *mine_base = lane < NV ? K : Vc;
+        int page = 0;
+        auto ask = [&](int k0) {  // the pages of a tile (behind the end: of the last key)
+            const int key = k0 + mine_top;
+            page = table[(unsigned)(key < end ? key : last) >> d.log_page];
+        };
+        uint64_t at = 0;
+        auto place = [&](int k0) {
+            at = (uint64_t)(mine_base + page_bound(d, page) * d.page_stride + ((k0 + mine_top) & (d.page - 1)) * D);
+        };
+        auto copy = [&](int buf, int i) {
+            const uint64_t base = (uint64_t)(unsigned)__builtin_amdgcn_readlane((int)(at >> 32), i) << 32 |
+                                  (unsigned)__builtin_amdgcn_readlane((int)at, i);
+            const int j = i % NV;
+            const unsigned to = (buf * KT * LINE + j * BLOCK + w * 64) * 16;
+            if (i < NV) copy_to_lds((const void *)base, from_of(j, TL::swap_k(row_of(j))), lds_k + to);
+            else copy_to_lds((const void *)base, from_of(j, TL::swap_v(row_of(j))), lds_v + to);
+        };
+        auto load = [&](int k0, int buf) {
+            place(k0);
+#pragma unroll
+            for (int i = 0; i < 2 * NV; ++i) copy(buf, i);
+        };
+        // V of a cut tile: rows behind the end and values that are not finite are made 0
+        auto clean = [&](int k0, int buf) {
             bool bad = false;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (tail && k0 + row_of(i) >= end) rv[i] = vec(0);  // whatever the cache holds there
+                const int x = i * BLOCK + tid, row = row_of(i);
+                vec v = ld16(&sv[buf][x * V]);
                 unsigned bits = 0;
 #pragma unroll
-                for (int j = 0; j < V; ++j) bits |= (unsigned)not_finite(rv[i][j]) << j;
-                if (bits) {
+                for (int j = 0; j < V; ++j) bits |= (unsigned)not_finite(v[j]) << j;
+                if (k0 + row >= end) bits = 0;  // (whatever the cache holds there)
 #pragma unroll
-                    for (int j = 0; j < V; ++j) rv[i][j] = bits >> j & 1 ? T(0.f) : rv[i][j];
-                }
+                for (int j = 0; j < V; ++j) v[j] = k0 + row >= end || (bits >> j & 1) ? T(0.f) : v[j];
+                st16(&sv[buf][x * V], v);
+                s_bits[buf][row * LINE + (x - row * LINE ^ TL::swap_v(row))] = (unsigned char)bits;
                 bad |= bits != 0;
-                s_bits[buf][i * BLOCK + tid] = (unsigned char)bits;
             }
             const bool any = __any(bad);
             if (lane == 0) s_bad[buf][w] = any;
+        };
+        if (begin < end) {
+            ask(begin);
+            load(begin, 0);
+            ask(begin + KT);
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            st16(&sk[buf][row_of(i) * TL::KP + col_of(i)], rk[i]);
-            st16(&sv[buf][row_of(i) * TL::VP + col_of(i)], rv[i]);
-        }
-    };
-    if (begin < end) {
-        // (behind the end the last row again and again: a branch would keep the old values beside the new)
-        ask(begin);
-        load(begin);
-        ask(begin + KT);
-        store(begin, 0);
-        load(begin + KT);
-        ask(begin + 2 * KT);
-    }
-    lds_sync();
 
-    int buf = 0;
-    for (int k0 = begin; k0 < end; k0 += KT, buf ^= 1) {
-        const bool mine = busy && k0 <= pw1 && k0 + KT > first_key(d, pw0);
-        acc sc[NT];
-        bool masked = false;
-        if (mine) {
+        auto met = [&](int buf) {
+            int x = 0;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) sc[t] = acc(0.f);
-            // product u: chunk u / NT of the channels, keys W (u % NT)..
-            auto key_rows = [&](int u) {
-                return *reinterpret_cast<const typename Frag16<T>::type *>(&sk[buf][(W * (u % NT) + c) * TL::KP + 8 * G * (u / NT) + 8 * h]);
-            };
-            constexpr int R = NT + TL::AHEAD;
-            frag kf[R];
-            acc taken[NT];  // (16 x 16: the sum is not updated in place)
-#pragma unroll
-            for (int u = 0; u < TL::AHEAD; ++u) kf[u] = key_rows(u);
-#pragma unroll
-            for (int u = 0; u < NC * NT; ++u) {
-                __builtin_amdgcn_sched_barrier(0);
-                if constexpr (W == 16) sc[u % NT] = MM::mma(kf[u % R], qf[u / NT], sc[u % NT], taken[u % NT]);
-                else sc[u % NT] = MM::mma(kf[u % R], qf[u / NT], sc[u % NT]);
-                __builtin_amdgcn_sched_barrier(0);
-                constexpr int LAST = NC * NT - TL::AHEAD - 1;  // of the steps that load
-                if (u <= LAST) kf[(u + TL::AHEAD) % R] = key_rows(u + TL::AHEAD);
-#pragma unroll
-                for (int v = 0; v <= u; ++v)  // operands of sums that no product has taken yet
-                    if (v == u - NT + 1 || (u == LAST && v > u - NT)) operand_in_use<T>(kf[v % R]);
-                if (W == 16) {
-#pragma unroll
-                    for (int t = 0; t < NT && t <= u; ++t) in_use(taken[t]);
-                }
+            for (int i = 0; i < TL::WAVES; ++i) x |= s_bad[buf][i];
+            return x != 0;
+        };
+        int buf = 0;
+        for (int k0 = begin; k0 < end; k0 += KT, buf ^= 1) {
+            wait_vmem_all();  // this wave's part of the tile has come
+            lds_sync();       // and every wave's; the other buffer has been read
+            place(k0 + KT);
+            ask(k0 + 2 * KT);
+            if (cut(k0)) {
+                clean(k0, buf);
+                lds_sync();
             }
-            masked = k0 + KT - 1 > pw0 || k0 < first_key(d, pw1);
-            if (masked) {
+            // copies of the next tile beside the scores' products from the second on, the rest after them
+            constexpr int START = 1, EVERY = (NC * NT - START) / (2 * NV) > 0 ? (NC * NT - START) / (2 * NV) : 1;
+            constexpr int BESIDE = (NC * NT - START + EVERY - 1) / EVERY < 2 * NV ? (NC * NT - START + EVERY - 1) / EVERY : 2 * NV;
+            const bool mine = busy && k0 <= pw1 && k0 + KT > first_key(d, pw0);
+            acc sc[NT];
+            bool masked = false;
+            if (mine) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) sc[t] = acc(0.f);
+                // product u: channels 8 G (u / NT).., keys W (u % NT)..
+                auto key_rows = [&](int u) {
+                    const T *row = &sk[buf][(W * (u % NT) + c) * D];
+                    const int x = (8 * G * (u / NT) + 8 * h) / V, swap = TL::swap_k(c);
+                    if constexpr (sizeof(T) == 4) {
+                        const f4 a = *reinterpret_cast<const f4 *>(row + (x ^ swap) * V), b = *reinterpret_cast<const f4 *>(row + ((x + 1) ^ swap) * V);
+                        return (frag)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+                    } else {
+                        return *reinterpret_cast<const frag *>(row + (x ^ swap) * V);
+                    }
+                };
+                __builtin_amdgcn_s_setprio(1);
+                constexpr int R = NT + TL::AHEAD;
+                frag kf[R];
+                acc taken[NT];  // (16 x 16: the sum is not updated in place)
+#pragma unroll
+                for (int u = 0; u < TL::AHEAD; ++u) kf[u] = key_rows(u);
+#pragma unroll
+                for (int u = 0; u < NC * NT; ++u) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (W == 16) sc[u % NT] = MM::mma(kf[u % R], qf[u / NT], sc[u % NT], taken[u % NT]);
+                    else sc[u % NT] = MM::mma(kf[u % R], qf[u / NT], sc[u % NT]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (u >= START && (u - START) % EVERY == 0 && (u - START) / EVERY < 2 * NV) copy(buf ^ 1, (u - START) / EVERY);
+                    constexpr int LAST = NC * NT - TL::AHEAD - 1;  // of the steps that load
+                    if (u <= LAST) kf[(u + TL::AHEAD) % R] = key_rows(u + TL::AHEAD);
+#pragma unroll
+                    for (int v = 0; v <= u; ++v)  // operands of sums that no product has taken yet
+                        if (v == u - NT + 1 || (u == LAST && v > u - NT)) operand_in_use<T>(kf[v % R]);
+                    if (W == 16) {
+#pragma unroll
+                        for (int t = 0; t < NT && t <= u; ++t) in_use(taken[t]);
+                    }
+                }
+                __builtin_amdgcn_s_setprio(0);
+                masked = k0 + KT - 1 > pw0 || k0 < first_key(d, pw1);
+                if (masked) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < NA; ++i) {
+                            const int key = k0 + W * t + 4 * G * (i >> 2) + 4 * h + (i & 3);
+                            sc[t][i] = key <= p && key >= low ? sc[t][i] : -INFINITY;
+                        }
+                }
+                float most = -INFINITY;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int i = 0; i < NA; ++i) {
-                        const int key = k0 + W * t + 4 * G * (i >> 2) + 4 * h + (i & 3);
-                        sc[t][i] = key <= p && key >= low ? sc[t][i] : -INFINITY;
+                    for (int i = 0; i < NA; ++i) most = fmaxf(most, sc[t][i]);
+                most = column_max<G>(most) * cs;
+                if (__any(most > m + 8.f)) {
+                    const float m1 = fmaxf(m, most), keep = __builtin_amdgcn_exp2f(m - (m1 == -INFINITY ? 0.f : m1));
+                    m = m1;
+                    l *= keep;
+#pragma unroll
+                    for (int t = 0; t < ND; ++t) o[t] *= keep;
+                }
+                if (cut(k0) && met(buf)) {  // (rare: no care for its time)
+#pragma unroll 1
+                    for (int j = 0; j < KT; ++j) {
+                        const bool sees = k0 + j <= p && k0 + j >= low && k0 + j < end;
+#pragma unroll
+                        for (int t = 0; t < ND; ++t)
+#pragma unroll
+                            for (int i = 0; i < UNITS; ++i) {
+                                const int ch = W * t + 4 * G * i + 4 * h;
+                                const unsigned bits = sees ? s_bits[buf][j * LINE + ch / V] >> (ch % V) & 15 : 0;
+                                dead[(t * NA + 4 * i) / 32] |= bits << (t * NA + 4 * i) % 32;
+                                __builtin_amdgcn_sched_barrier(0);
+                            }
                     }
+                }
             }
-            float most = -INFINITY;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int i = BESIDE; i < 2 * NV; ++i) copy(buf ^ 1, i);
+            if (!mine) {
 #pragma unroll
-                for (int i = 0; i < NA; ++i) most = fmaxf(most, sc[t][i]);
-            most = column_max<G>(most) * cs;
-            if (__any(most > m + 8.f)) {
-                const float m1 = fmaxf(m, most), keep = __builtin_amdgcn_exp2f(m - (m1 == -INFINITY ? 0.f : m1));
-                m = m1;
-                l *= keep;
-#pragma unroll
-                for (int t = 0; t < ND; ++t) o[t] *= keep;
+                for (int i = 0; i < BESIDE; ++i) copy(buf ^ 1, i);
             }
-            if (cut(k0) && (s_bad[buf][0] | s_bad[buf][1] | s_bad[buf][2] | s_bad[buf][3])) {  // (rare: no care for its time)
-                for (int j = 0; j < KT; ++j) {
-                    const bool sees = k0 + j <= p && k0 + j >= low && k0 + j < end;
+            if (mine) {
+                // product u: channels W (u % ND).., keys 8 G (u / ND)..
+                auto channels = [&](int u) { return column<T, D>(sv[buf], u / ND, u % ND, lane); };
+                constexpr int R = ND + TL::AHEAD;
+                frag vf[R];
+                acc held[ND];
+#pragma unroll
+                for (int u = 0; u < TL::AHEAD; ++u) vf[u] = channels(u);
+                const float m0 = m == -INFINITY ? 0.f : m;
+                frag pf[NK];
+#pragma unroll
+                for (int k = 0; k < NK; ++k) {
+                    float wt[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int at = 2 * k + (i >> 2);  // in units of 4 G keys
+                        wt[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[at / UNITS][at % UNITS * 4 + (i & 3)], cs, -m0));
+                        l += wt[i];
+                    }
+                    frag one[1];
+                    split8<T, 1>(wt, one);
+                    pf[k] = one[0];
+                    __builtin_amdgcn_sched_barrier(0);  // (or all the weights live at once)
+                }
+                __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+                for (int u = 0; u < NK * ND; ++u) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (sizeof(T) == 4) o[u % ND] = MM::mma(vf[u % R], pf[u / ND], o[u % ND], held[u % ND]);
+                    else o[u % ND] = MM::mma(vf[u % R], pf[u / ND], o[u % ND]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    constexpr int LAST = NK * ND - TL::AHEAD - 1;
+                    if (u <= LAST) vf[(u + TL::AHEAD) % R] = channels(u + TL::AHEAD);
+#pragma unroll
+                    for (int v = 0; v <= u; ++v)
+                        if (v == u - ND + 1 || (u == LAST && v > u - ND)) operand_in_use<T>(vf[v % R]);
+                    if (sizeof(T) == 4 && u <= LAST) {
+#pragma unroll
+                        for (int t = 0; t < ND && t <= u; ++t) in_use(held[t]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < NK; ++k) operand_in_use<T>(pf[k]);
+                __builtin_amdgcn_s_setprio(0);
+            }
+        }
+
+        l = column_sum<G>(l);
+        wait_vmem_all();  // (the copy of the tile behind the last one)
+        if (r < used) {
+#pragma unroll
+            for (int t = 0; t < ND; ++t)
+#pragma unroll
+                for (int i = 0; i < NA; ++i) o[t][i] = dead[(t * NA + i) / 32] >> (t * NA + i) % 32 & 1 ? NAN : o[t][i];
+            if (!LINED || whole) {
+                const float inv = inverse_sum(l);
+                typename Quad<T>::t4 gate[ND][UNITS] = {};  // (all asked for before the first store)
+                if (s.a.gate) {
 #pragma unroll
                     for (int t = 0; t < ND; ++t)
 #pragma unroll
-                        for (int i = 0; i < UNITS; ++i) {
-                            const int ch = W * t + 4 * G * i + 4 * h;
-                            const unsigned bits = sees ? s_bits[buf][(j * D + ch) / V] >> (ch % V) & 15 : 0;
-                            dead[(t * NA + 4 * i) / 32] |= bits << (t * NA + 4 * i) % 32;
-                            __builtin_amdgcn_sched_barrier(0);
-                        }
+                        for (int i = 0; i < UNITS; ++i) gate[t][i] = gate_of<T>(d, s.a, b.row + tok, head, W * t + 4 * G * i + 4 * h);
                 }
+#pragma unroll
+                for (int t = 0; t < ND; ++t)
+#pragma unroll
+                    for (int i = 0; i < UNITS; ++i) {
+                        const f4 x = {o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
+                        finish<T>(d, s.a, b.row + tok, head, W * t + 4 * G * i + 4 * h, x, inv, gate[t][i]);
+                    }
+            } else {
+                const int64_t piece = 2 * (int64_t)blockIdx.x + (ch == 0);
+                if (h == 0) s.ml[piece * TL::ROWS + r] = make_float2(m, l);
+#pragma unroll
+                for (int t = 0; t < ND; ++t)
+#pragma unroll
+                    for (int i = 0; i < UNITS; ++i) {
+                        const f4 x = {o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
+                        s.o[((piece * TL::WAVES + w) * ND * UNITS + t * UNITS + i) * 64 + lane] = x;  // whole lines
+                    }
             }
         }
-        // the next tile goes to the other buffer, the one after it is asked for
-        __builtin_amdgcn_sched_barrier(0);
-        store(k0 + KT, buf ^ 1);
-        load(k0 + 2 * KT);
-        ask(k0 + 3 * KT);
-        if (mine) {
-            // product u: channels W (u % ND).., keys 8 G (u / ND)..
-            auto channels = [&](int u) { return column<T, W, TL::VP>(sv[buf], u / ND, u % ND, lane); };
-            constexpr int R = ND + TL::AHEAD;
-            frag vf[R];
-            acc held[ND];
-#pragma unroll
-            for (int u = 0; u < TL::AHEAD; ++u) vf[u] = channels(u);
-            const float m0 = m == -INFINITY ? 0.f : m;
-            frag pf[NK];
-#pragma unroll
-            for (int k = 0; k < NK; ++k) {
-                float wt[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int at = 2 * k + (i >> 2);  // in units of 4 G keys
-                    wt[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[at / UNITS][at % UNITS * 4 + (i & 3)], cs, -m0));
-                    l += wt[i];
-                }
-                frag one[1];
-                split8<T, 1>(wt, one);
-                pf[k] = one[0];
-                __builtin_amdgcn_sched_barrier(0);  // (or all the weights live at once)
-            }
-#pragma unroll
-            for (int u = 0; u < NK * ND; ++u) {
-                __builtin_amdgcn_sched_barrier(0);
-                if constexpr (sizeof(T) == 4) o[u % ND] = MM::mma(vf[u % R], pf[u / ND], o[u % ND], held[u % ND]);
-                else o[u % ND] = MM::mma(vf[u % R], pf[u / ND], o[u % ND]);
-                __builtin_amdgcn_sched_barrier(0);
-                constexpr int LAST = NK * ND - TL::AHEAD - 1;
-                if (u <= LAST) vf[(u + TL::AHEAD) % R] = channels(u + TL::AHEAD);
-#pragma unroll
-                for (int v = 0; v <= u; ++v)
-                    if (v == u - ND + 1 || (u == LAST && v > u - ND)) operand_in_use<T>(vf[v % R]);
-                if (sizeof(T) == 4 && u <= LAST) {
-#pragma unroll
-                    for (int t = 0; t < ND && t <= u; ++t) in_use(held[t]);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < NK; ++k) operand_in_use<T>(pf[k]);
-        }
-        lds_sync();
-    }
-
-    l = column_sum<G>(l);
-    if (r >= used) return;
-#pragma unroll
-    for (int t = 0; t < ND; ++t)
-#pragma unroll
-        for (int i = 0; i < NA; ++i) o[t][i] = dead[(t * NA + i) / 32] >> (t * NA + i) % 32 & 1 ? NAN : o[t][i];
-    if (whole) {
-        const float inv = inverse_sum(l);
-#pragma unroll
-        for (int t = 0; t < ND; ++t)
-#pragma unroll
-            for (int i = 0; i < UNITS; ++i) {
-                const f4 x = {o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
-                finish<T>(d, s.a, b.row + tok, head, W * t + 4 * G * i + 4 * h, x, inv);
-            }
-    } else {
-        const int64_t at = (((int64_t)slot * gridDim.y + blockIdx.y) * s.pieces + blockIdx.z) * TL::ROWS + r;
-        if (h == 0) s.ml[at] = make_float2(m, l);
-#pragma unroll
-        for (int t = 0; t < ND; ++t)
-#pragma unroll
-            for (int i = 0; i < UNITS; ++i) {
-                const f4 x = {o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
-                *reinterpret_cast<f4 *>(s.o + at * D + W * t + 4 * G * i + 4 * h) = x;
-            }
+        if constexpr (!LINED) return;
+        pos += count;
+        lds_sync();  // every wave has read its last tile
     }
 }
 
-// The rows whose keys were cut: a thread 4 channels of a row
+// The rows that the line is cut in: a block a cut and 1024 values.  The first cut of a row's keys stands
+// for all; the others leave.
 template <typename T, int D>
-__global__ __launch_bounds__(BLOCK) void join_kernel(AttnDims d, PrefillArgs s)
+__global__ __launch_bounds__(256) void join_kernel(AttnDims d, PrefillArgs s)
 {
-    constexpr int LANES = D / 4, KT = Tile<T, D>::KT, ROWS = Tile<T, D>::ROWS;
-    const int slot = blockIdx.x;
-    const int kh = blockIdx.y / s.parts, head0 = kh * d.g + (blockIdx.y - kh * s.parts) * s.heads;
+    typedef Tile<T, D> TL;
+    constexpr int KT = TL::KT, ROWS = TL::ROWS, W = TL::W, G = TL::G, UNITS = TL::NA / 4;
+    const int64_t part = blockIdx.x + 1;
+    const Place pl = s.place[part];
+    if (pl.slot < 0 || pl.ch == 0 || (unsigned)pl.ch > pl.quantum) return;
+    const int kh = pl.hy / s.parts, head0 = kh * d.g + (pl.hy - kh * s.parts) * s.heads;
     const int g = (kh + 1) * d.g - head0 < s.heads ? (kh + 1) * d.g - head0 : s.heads;
     Work b;
-    if (!locate<KT>(d, s, slot, b)) return;
-    const int n = (b.end - b.begin + s.piece - 1) / s.piece;
-    if (n <= 1) return;
-    const int i = blockIdx.z * BLOCK + threadIdx.x, r = i / LANES, col = (i - r * LANES) * 4;
+    if (!locate<KT>(d, s, pl.slot, b)) return;
+    const int at = blockIdx.y * 256 + threadIdx.x, lane = at % 64, unit = at / 64 % (D * W / 256), w = at / 64 / (D * W / 256);
+    const int r = W * w + lane % W, col = W * (unit / UNITS) + 4 * G * (unit % UNITS) + 4 * (lane / W);
     if (r >= b.tokens * g) return;
-    const int64_t at = ((int64_t)slot * gridDim.y + blockIdx.y) * s.pieces * ROWS + r;
+    const int n = 1 + (int)((pl.nc - pl.ch + (int64_t)pl.quantum - 1) / pl.quantum);
+    // the first piece is the end of part - 1, the others begin in their part
+    auto piece = [&](int u) { return u == 0 ? 2 * (part - 1) + 1 : 2 * (part - 1 + u); };
     float big = -INFINITY;
-    for (int u = 0; u < n; ++u) big = fmaxf(big, s.ml[at + (int64_t)u * ROWS].x);
+    for (int u = 0; u < n; ++u) big = fmaxf(big, s.ml[piece(u) * ROWS + r].x);
     const float big0 = big == -INFINITY ? 0.f : big;
     float l = 0.f;
     f4 sum = f4(0.f);
 #pragma unroll 4
     for (int u = 0; u < n; ++u) {
-        const float2 x = s.ml[at + (int64_t)u * ROWS];
+        const float2 x = s.ml[piece(u) * ROWS + r];
         const float f = __builtin_amdgcn_exp2f(x.x - big0);
         l += f * x.y;
-        sum += f * *reinterpret_cast<const f4 *>(s.o + (at + (int64_t)u * ROWS) * D + col);
+        sum += f * s.o[piece(u) * (ROWS * D / 4) + at];
     }
-    const int tok = r / g;
-    finish<T>(d, s.a, b.row + tok, head0 + r - tok * g, col, sum, inverse_sum(l));
+    const int tok = r / g, head = head0 + r - tok * g;
+    typename Quad<T>::t4 gate = {};
+    if (s.a.gate) gate = gate_of<T>(d, s.a, b.row + tok, head, col);
+    finish<T>(d, s.a, b.row + tok, head, col, sum, inverse_sum(l), gate);
 }
 
-// Keys are cut where a launch would have less than 512 blocks (two a CU), into
-// pieces of 512 at least.
+// The line costs about 15 us for its join and one more start and end of rows a block; it is taken where the launch
+// would have fewer blocks than are resident at once, and the keys that the idle ones could take are more
+// than LINE_KEYS for each: 64 tokens after 1000 23 us with it and 45 without; 900 from their start 48 and 42; 1024 tokens
+// of 32 heads of 128 51 and 29.
+constexpr int64_t LINE_KEYS = 640;
 struct Plan {
-    int heads, parts, tokens, slots, pieces, piece;
-    size_t ml, o;
+    int heads, parts, tokens, slots, line;
+    size_t place, ml, o;
 };
-Plan plan_of(const AttnDims &d, int rows)
+Plan plan_of(const AttnDims &d, int rows, int on_cu)
 {
     Plan p;
     p.heads = d.g < rows ? d.g : rows;
@@ -550,27 +736,30 @@ Plan plan_of(const AttnDims &d, int rows)
     p.slots = (int)(d.T / p.tokens) + d.n_seq;
     const int64_t blocks = (int64_t)p.slots * d.KV * p.parts;
     int64_t span = d.max_kv;
-    if (d.window < span) span = (int64_t)d.window + p.tokens + 64 < span ? (int64_t)d.window + p.tokens + 64 : span;
-    int64_t piece = span * blocks / 512;
-    piece = (piece < 512 ? 512 : piece) / 64 * 64 + 64;
-    p.pieces = blocks >= 512 || span <= piece ? 1 : (int)((span + 64 + piece - 1) / piece);
-    p.piece = p.pieces == 1 ? INT32_MAX / 2 : (int)piece;
-    const size_t cut = p.pieces == 1 ? 0 : (size_t)blocks * p.pieces * rows;
-    p.ml = (cut * sizeof(float2) + 255) / 256 * 256;
-    p.o = cut * d.D * sizeof(float);
+    if (d.window < span && (int64_t)d.window + p.tokens + 64 < span) span = (int64_t)d.window + p.tokens + 64;
+    const int64_t most = blocks * ((span + CHUNK - 1) / CHUNK + 1);
+    p.line = 0;
+    const int64_t resident = 256 * on_cu;
+    if (blocks < resident && p.slots <= MOST_SLOTS && span * (resident - blocks) > LINE_KEYS * resident)
+        p.line = (int)(most < resident ? most : resident);
+    p.place = ((size_t)p.line * sizeof(Place) + 255) / 256 * 256;
+    p.ml = (size_t)p.line * 2 * rows * sizeof(float2);
+    p.o = (size_t)p.line * 2 * rows * d.D * sizeof(float);
     return p;
 }
 
 template <typename T, int D>
 void launch_prefill_t(const AttnDims &d, const AttnArgs &a, hipStream_t st)
 {
-    constexpr int ROWS = Tile<T, D>::ROWS;
-    const Plan p = plan_of(d, ROWS);
-    const PrefillArgs s{a, p.heads, p.parts, p.tokens, p.slots, p.pieces, p.piece, static_cast<float2 *>(a.ws),
-                        reinterpret_cast<float *>(static_cast<char *>(a.ws) + p.ml)};
-    hipLaunchKernelGGL((prefill_kernel<T, D>), dim3(s.slots, d.KV * s.parts, s.pieces), dim3(BLOCK), 0, st, d, s);
-    if (s.pieces > 1)
-        hipLaunchKernelGGL((join_kernel<T, D>), dim3(s.slots, d.KV * s.parts, ROWS * (D / 4) / BLOCK), dim3(BLOCK), 0, st, d, s);
+    typedef Tile<T, D> TL;
+    const Plan p = plan_of(d, TL::ROWS, TL::BLOCKS);
+    char *ws = static_cast<char *>(a.ws);
+    const PrefillArgs s{a, p.heads, p.parts, p.tokens, p.slots, p.line, reinterpret_cast<Place *>(ws),
+                        reinterpret_cast<float2 *>(ws + p.place), reinterpret_cast<f4 *>(ws + p.place + p.ml)};
+    const int gy = p.slots < 32768 ? p.slots : 32768;
+    const dim3 grid = p.line ? dim3(p.line) : dim3(d.KV * p.parts, gy, (p.slots + gy - 1) / gy);
+    hipLaunchKernelGGL((p.line ? prefill_kernel<T, D, true> : prefill_kernel<T, D, false>), grid, dim3(TL::BLOCK), 0, st, d, s);
+    if (p.line > 1) hipLaunchKernelGGL((join_kernel<T, D>), dim3(p.line - 1, TL::ROWS * (D / 4) / 256), dim3(256), 0, st, d, s);
 }
 
 #define GDN_ATTN_D(...)                                    \
@@ -586,10 +775,10 @@ void launch_prefill_t(const AttnDims &d, const AttnArgs &a, hipStream_t st)
 
 size_t attn_prefill_workspace_bytes(const gdn_attn_shape &s)
 {
-    int rows = 0;
-    GDN_SSM_IO(s.io_dtype, GDN_ATTN_D(rows = Tile<TI, D>::ROWS;))
-    const Plan p = plan_of(attn_dims(s), rows);
-    return p.ml + p.o;
+    int rows = 0, blocks = 0;
+    GDN_SSM_IO(s.io_dtype, GDN_ATTN_D(rows = Tile<TI, D>::ROWS; blocks = Tile<TI, D>::BLOCKS;))
+    const Plan p = plan_of(attn_dims(s), rows, blocks);
+    return p.place + p.ml + p.o;
 }
 
 hipError_t launch_attn_prefill(const gdn_attn_shape &s, const AttnArgs &a, hipStream_t st)

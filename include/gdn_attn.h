@@ -71,7 +71,7 @@ extern "C" {
 /* Sizes of one call.  Supported: 1 <= kv_heads, heads % kv_heads == 0,
  * heads / kv_heads <= 128, heads <= 4096; head_dim 64, 96, 128, 192 or 256;
  * page_size a power of two from 16 to 1024; 1 <= n_seq <= 65536; 0 <= max_T <=
- * total_T <= 2^27; 1 <= n_pages; 1 <= table_pages; 0 <= max_kv <= 2^30 and
+ * total_T <= 2^26; 1 <= n_pages; 1 <= table_pages; 0 <= max_kv <= 2^30 and
  * max_kv <= table_pages * page_size; strides 0 or a row's (page's) elements up
  * to 2^40; n_pages * page_stride <= 2^56; rope_dim a multiple of 16 up to
  * head_dim; window >= 0; scale > 0, rope_scale and eps >= 0, all finite.
