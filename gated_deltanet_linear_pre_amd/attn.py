@@ -79,21 +79,25 @@ _TORCH = {GDN_F32: torch.float32, GDN_F16: torch.float16, GDN_BF16: torch.bfloat
 
 @functools.lru_cache(maxsize=256)
 def _plan(name: str, raw: bytes):
-    """(argument, type, elements, stride, count) of a call's tensors, from the bytes of its
-    shape.  stride None: a tensor without gaps, of that many elements; else `count` rows or
-    pages of `elements` each, that far apart."""
+    """(argument, type, least elements, natural sizes, natural strides, piece) of a call's
+    tensors, from the bytes of its shape.  A tensor without gaps needs the elements, any other
+    the sizes and strides; of other views _refuse looks at the piece: elements, stride and
+    count of its rows or pages (None: it has to be without gaps)."""
     s = gdn_attn_shape.from_buffer_copy(raw)
     io, f32, i32 = _TORCH.get(s.io_dtype), torch.float32, torch.int32
     T, D, q, kv = s.total_T, s.head_dim, s.heads * s.head_dim, s.kv_heads * s.head_dim
-    page = kv * s.page_size
 
     def flat(arg, dtype, least):
-        return arg, dtype, least, None, 1
+        return arg, dtype, least, None, None, None
 
     def rows(arg, cols, stride):
-        return arg, io, cols, stride or cols, T
+        stride = stride or cols
+        return arg, io, (T - 1) * stride + cols if T > 0 else 0, (T, cols), (stride, 1), (cols, stride, T)
 
-    cache = tuple((k, io, page, s.page_stride or page, s.n_pages) for k in ("k_cache", "v_cache"))
+    page = kv * s.page_size
+    stride = s.page_stride or page
+    cache = tuple((k, io, (s.n_pages - 1) * stride + page, (s.n_pages, s.kv_heads, s.page_size, D),
+                   (stride, s.page_size * D, D, 1), (page, stride, s.n_pages)) for k in ("k_cache", "v_cache"))
     if name == "gdn_attn_copy_pages":
         return (flat("pairs", i32, 0), *cache)
     seqs = (flat("kv_len", i32, s.n_seq), flat("page_table", i32, s.n_seq * s.table_pages))
@@ -104,7 +108,7 @@ def _plan(name: str, raw: bytes):
                 flat("inv_freq", f32, s.rope_dim // 2), flat("q_norm", io, D), flat("k_norm", io, D), flat("q_out", io, T * q),
                 *cache)
     return (*seqs, rows("q", q, s.q_stride), *cache, rows("gate", q, s.gate_stride), flat("out", io, T * q),
-            flat("workspace", None, 0))
+            flat("workspace", torch.uint8, 0))
 
 
 def _dense(x) -> bool:
@@ -117,23 +121,20 @@ def _dense(x) -> bool:
     return True
 
 
-def _refuse(name: str, x, arg, dtype, size, stride, count):
+def _refuse(name: str, x, arg, dtype, least, piece):
     """ValueError if `x` is not the tensor of this entry of the plan; _call comes here with
     what is not so at first sight."""
-    if dtype is not None and x.dtype is not dtype:
+    if x.dtype is not dtype and arg != "workspace":  # (bytes of any type)
         raise ValueError(f"{name}: {arg} is {x.dtype}, the shape says {dtype}")
-    if stride is None:
+    if piece is None or x.is_contiguous():
         if not x.is_contiguous():
             raise ValueError(f"{name}: {arg} has gaps between its elements (strides {x.stride()})")
-        if x.numel() < size:
-            raise ValueError(f"{name}: {arg} has {x.numel()} elements of {size}")
+        if x.numel() < least:
+            raise ValueError(f"{name}: {arg} has {x.numel()} elements of {least}")
         return
-    if x.is_contiguous():
-        fits = count <= 0 or x.numel() >= (count - 1) * stride + size
-    else:
-        n = x.shape[0] if x.dim() else 0
-        fits = x.dim() >= 2 and n >= count and (n == 0 or x.numel() // n >= size) and _dense(x) and (count <= 1 or x.stride(0) == stride)
-    if not fits:
+    size, stride, count = piece
+    n = x.shape[0] if x.dim() else 0
+    if x.dim() < 2 or n < count or n > 0 and x.numel() // n < size or not _dense(x) or count > 1 and x.stride(0) != stride:
         raise ValueError(f"{name}: {arg} of {tuple(x.shape)}, strides {x.stride()}, is not {count} pieces of {size} elements, {stride} apart")
 
 
@@ -141,13 +142,13 @@ def _call(name: str, shape, tensors, tail, stream, check: bool, between=()) -> i
     """One library call: addresses (`between` after the first of them), then `tail`, then the stream."""
     dev = -1
     args = []
-    for x, (arg, dtype, size, stride, count) in zip(tensors, _plan(name, bytes(shape))):
+    for x, (arg, dtype, least, sizes, strides, piece) in zip(tensors, _plan(name, bytes(shape))):
         if x is None or type(x) is int:
             args.append(x)
             continue
-        if x.dtype is not dtype or not (x.is_contiguous() and x.numel() >= size if stride is None
-                                        else x.dim() == 2 and x.stride() == (stride, 1) and x.shape == (count, size)):
-            _refuse(name, x, arg, dtype, size, stride, count)
+        if x.dtype is not dtype or not (x.numel() >= least if x.is_contiguous()
+                                        else x.stride() == strides and x.shape == sizes):
+            _refuse(name, x, arg, dtype, least, piece)
         at = x.get_device()
         if at != dev or at < 0:
             if at < 0:
