@@ -145,29 +145,6 @@ struct Place {
     unsigned quantum;
 };
 
-__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
-
-// 4 channels of an output row: its gate's values, and o r, gated
-template <typename T> struct Quad {
-    typedef T t4 __attribute__((ext_vector_type(4)));
-};
-template <typename T>
-__device__ __forceinline__ typename Quad<T>::t4 gate_of(const AttnDims &d, const AttnArgs &a, int64_t row, int head, int col)
-{
-    return *reinterpret_cast<const typename Quad<T>::t4 *>(static_cast<const T *>(a.gate) + row * d.gate_stride + head * d.D + col);
-}
-template <typename T>
-__device__ __forceinline__ void finish(const AttnDims &d, const AttnArgs &a, int64_t row, int head, int col, f4 o, float r,
-                                       typename Quad<T>::t4 gate)
-{
-    typename Quad<T>::t4 y;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = (T)(a.gate ? o[i] * r * __builtin_amdgcn_rcpf(1.0f + exp_fast(-(float)gate[i])) : o[i] * r);
-    *reinterpret_cast<typename Quad<T>::t4 *>(static_cast<T *>(a.out) + (row * d.H + head) * d.D + col) = y;
-}
-// 1 / sum of weights; no key: o and the sum are 0 (a NaN stays one)
-__device__ __forceinline__ float inverse_sum(float l) { return l > 0.f ? 1.0f / l : l; }
-
 // over the G lanes of a column
 template <int G>
 __device__ __forceinline__ float column_max(float x)

@@ -6,7 +6,7 @@
 // a matrix product (a unit: sequence, key-value head, 16 query heads), and K and V
 // are read once: bound by HBM bandwidth.
 //
-// Work.  The keys of all units, in chunks of 128, form one line that is cut into equal
+// Work.  The keys of all units, in chunks of 64, form one line that is cut into equal
 // parts, one a block: every block finds its place by a prefix sum over kv_len, so the
 // parts are equal whatever the lengths are, also in a captured call whose lengths
 // have grown.  A block walks the segments (units, or pieces of them) of its part.  A
@@ -14,17 +14,22 @@
 // maximum and weights' sum in the workspace (a part cuts two units at most, at its
 // ends), and a second kernel joins them.
 //
-// gfx950 mapping.  Within a segment the block's 4 waves take tiles of KT keys in turn,
-// each on its own, with no barrier.  S^T = K Q^T puts a key a row and a query a
+// gfx950 mapping.  256 parts, one a CU (512 parts: 4 us more for their joins and ends), of 8 waves (4
+// of twice the registers where a head is wide) that take tiles of KT keys in turn, each on its own, with no
+// barrier.  S^T = K Q^T puts a key a row and a query a
 // column: the columns' maxima and sums stay in their lanes, and the weights of lane
 // (gq, c) are keys 4 gq + 0..3 of a tile, which is at once the operand of O^T = V^T w
 // if V^T is read in the same order of keys.  K goes from memory to the operands
 // directly; V through LDS, whose transposing reads give 4 keys of a channel a lane.
-// While a tile is computed the next one's K and V are loaded to registers.
+// While a tile is computed the next one's K and V are loaded to registers; they are read once, so
+// past the caches' order (83 us with it for what takes 76 without).
 //
 // Precision.  Scores, maxima, sums and O are fp32.  16-bit weights enter the product
 // with V in two parts of the matrix type (2^-16 of a weight at bf16, 2^-22 at fp16, or
 // 2^-25 of the largest): the matrix pipes have the time.
+//
+// Measured: one sequence of 99991 keys, 32 heads of 128 over 8, fp16, 73 us (5.6 TB/s); 64 sequences of up to
+// 20011 keys, 16 heads of 256 over 2, bf16, 88 us (4.7 TB/s); one of 701 keys 11 us.
 #include "attn_device.h"
 #include "mfma_device.h"
 
@@ -32,23 +37,22 @@ namespace gdn {
 
 namespace {
 
-constexpr int BLOCK = 256, WAVES = 4;
-constexpr int CHUNK = 128;   // keys that a unit is cut at
-constexpr int PARTS_MAX = 512;  // blocks of a launch
+constexpr int CHUNK = 64;       // keys that a unit is cut at
+constexpr int PARTS_MAX = 256;  // blocks of a launch
 
-// What a part leaves of its place for the kernel that joins: the chunk its first
-// sequence begins at, that sequence (-1: the part is empty), chunks of a part
-struct Place {
-    int64_t base, quantum;
-    int n, pad;
+// A unit that is cut, for the kernel that joins: its sequence and place in it, the part it begins in, and
+// how many parts have a piece (0: it is not cut)
+struct Cut {
+    int n, unit, first, pieces;
 };
 
 struct StepArgs {
     AttnArgs a;
-    int tiles;      // of 16 query heads in a key-value head
-    Place *place;   // [parts]
-    float2 *ml;     // [2 parts][16] maximum (of scores times scale log2 e) and sum of weights
-    float *o;       // [2 parts][16][D]
+    int tiles;     // of 16 query heads in a key-value head
+    bool by_unit;  // there are no more units than parts: cuts are listed by unit, else by the part they begin in
+    Cut *cut;      // [parts]
+    float2 *ml;    // [2 parts][16] maximum (of scores times scale log2 e) and sum of weights
+    float *o;      // [2 parts][16][D]
 };
 
 __device__ __forceinline__ int chunks_of(const AttnDims &d, int len)
@@ -60,6 +64,8 @@ __device__ __forceinline__ int chunks_of(const AttnDims &d, int len)
 template <typename T, int D> struct Tile {
     static constexpr int KT = sizeof(T) == 2 ? 32 : 16;  // keys
     static constexpr int NT = KT / 16, NC = D / 32, ND = D / 16;
+    static constexpr int WAVES = D <= 128 ? 8 : 4;
+    static constexpr int PER_SIMD = D <= 128 ? 2 : 1;  // waves
     static constexpr int V = Vec16<T>::n;
     static constexpr int NV = KT * D / V / 64;      // vectors of V a lane
     static constexpr int PITCH = D + 32 / sizeof(T);  // of V in LDS: 16 rows of 32 bytes then lie in 8 different groups of banks
@@ -119,27 +125,16 @@ __device__ __forceinline__ float sum_of_groups(float x)
     return x + __shfl_xor(x, 32, 64);
 }
 
-// out = o / l, gated, 4 channels
-template <typename T>
-__device__ __forceinline__ void finish(const AttnDims &d, const AttnArgs &a, int64_t row, int head, int col, f4 o, float l)
+// a / b of numbers that nearly always fit in 32 bits
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
 {
-    typedef T t4 __attribute__((ext_vector_type(4)));
-    const float r = l > 0.f ? 1.0f / l : l;  // no key: o and l are 0 (a NaN stays one)
-    t4 y;
-    if (a.gate) {
-        const t4 gate = *reinterpret_cast<const t4 *>(static_cast<const T *>(a.gate) + row * d.gate_stride + head * d.D + col);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = (T)(o[i] * r / (1.0f + expf(-(float)gate[i])));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = (T)(o[i] * r);
-    }
-    *reinterpret_cast<t4 *>(static_cast<T *>(a.out) + (row * d.H + head) * d.D + col) = y;
+    return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(BLOCK, D <= 128 ? 2 : 1) void step_kernel(AttnDims d, StepArgs s)
+__global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) void step_kernel(AttnDims d, StepArgs s)
 {
+    constexpr int WAVES = Tile<T, D>::WAVES, BLOCK = 64 * WAVES;
     typedef Mat<T> MT;
     typedef typename MT::frag frag;
     typedef Tile<T, D> TL;
@@ -172,11 +167,11 @@ __global__ __launch_bounds__(BLOCK, D <= 128 ? 2 : 1) void step_kernel(AttnDims 
         if (i < w) upto += s_wave[i];
         total += s_wave[i];
     }
-    const int64_t quantum = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t quantum = quotient(total + gridDim.x - 1, gridDim.x);
     int64_t pos = blockIdx.x * quantum;
     const int64_t stop = pos + quantum < total ? pos + quantum : total;
     if (pos >= total) {
-        if (tid == 0) s.place[blockIdx.x].n = -1;
+        if (tid == 0 && !s.by_unit) s.cut[blockIdx.x].pieces = 0;
         return;
     }
     if (pos >= upto - mine && pos < upto) {
@@ -189,7 +184,6 @@ __global__ __launch_bounds__(BLOCK, D <= 128 ? 2 : 1) void step_kernel(AttnDims 
         }
         s_base = base;
         s_n = n;
-        s.place[blockIdx.x] = Place{base, quantum, n, 0};
     }
     __syncthreads();
     int64_t base = s_base;
@@ -207,7 +201,7 @@ __global__ __launch_bounds__(BLOCK, D <= 128 ? 2 : 1) void step_kernel(AttnDims 
             ++n;
             continue;
         }
-        const int unit = (int)(local / nc), ch = (int)(local - (int64_t)unit * nc);
+        const int unit = (int)quotient(local, nc), ch = (int)(local - (int64_t)unit * nc);
         const int count = stop - pos < nc - ch ? (int)(stop - pos) : nc - ch;
         const int kh = unit / s.tiles, head0 = kh * d.g + (unit - kh * s.tiles) * 16;
         const int rows = (kh + 1) * d.g - head0 < 16 ? (kh + 1) * d.g - head0 : 16;
@@ -222,6 +216,16 @@ __global__ __launch_bounds__(BLOCK, D <= 128 ? 2 : 1) void step_kernel(AttnDims 
             if (c < rows) {
                 const T *p = static_cast<const T *>(s.a.q) + (int64_t)n * d.q_stride + (int64_t)(head0 + c) * D + 32 * i + 8 * gq;
                 qf[i] = *reinterpret_cast<const typename Frag16<T>::type *>(p);
+            }
+        }
+        const bool whole = count == nc;
+        constexpr int NR = (16 * (D / 4) + BLOCK - 1) / BLOCK;
+        typename Quad<T>::t4 gate[NR] = {};
+        if (whole && s.a.gate) {
+#pragma unroll
+            for (int u = 0; u < NR; ++u) {
+                const int i = u * BLOCK + tid, r = i / (D / 4);
+                if (r < rows) gate[u] = gate_of<T>(d, s.a, n, head0 + r, (i - r * (D / 4)) * 4);
             }
         }
         f4 o[ND];
@@ -246,12 +250,12 @@ __global__ __launch_bounds__(BLOCK, D <= 128 ? 2 : 1) void step_kernel(AttnDims 
             for (int t = 0; t < NT; ++t) {
                 const T *p = K + __shfl((long long)at, 16 * t + c, 64) + 8 * gq;
 #pragma unroll
-                for (int i = 0; i < NC; ++i) kf[t][i] = *reinterpret_cast<const typename Frag16<T>::type *>(p + 32 * i);
+                for (int i = 0; i < NC; ++i) kf[t][i] = __builtin_nontemporal_load(reinterpret_cast<const typename Frag16<T>::type *>(p + 32 * i));
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int x = i * 64 + lane, r = x / (D / V);
-                vv[i] = ld16(Vc + __shfl((long long)at, r, 64) + (x - r * (D / V)) * V);
+                vv[i] = __builtin_nontemporal_load(reinterpret_cast<const vec *>(Vc + __shfl((long long)at, r, 64) + (x - r * (D / V)) * V));
             }
         };
         int k0 = begin + w * KT;
@@ -315,7 +319,7 @@ __global__ __launch_bounds__(BLOCK, D <= 128 ? 2 : 1) void step_kernel(AttnDims 
             else weigh<D>(sv, wt, lane, o);
         }
 
-        // ---- the four waves' sums joined ----
+        // ---- the waves' sums joined ----
         l = sum_of_groups(l);
         __syncthreads();  // V has been read
         if (gq == 0) {
@@ -325,22 +329,30 @@ __global__ __launch_bounds__(BLOCK, D <= 128 ? 2 : 1) void step_kernel(AttnDims 
 #pragma unroll
         for (int t = 0; t < ND; ++t) *reinterpret_cast<f4 *>(so + c * TL::OP + 16 * t + 4 * gq) = o[t];
         __syncthreads();
-        const bool whole = count == nc;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (ch == 0);
-        for (int i = tid; i < rows * (D / 4); i += BLOCK) {
-            const int r = i / (D / 4), col = (i - r * (D / 4)) * 4;
-            const float big = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r]));
+        if (tid == 0 && (s.by_unit ? ch == 0 : pos + count == stop)) {
+            const int64_t later = ch == 0 ? nc - count : 0;
+            s.cut[s.by_unit ? n * units + unit : (int)blockIdx.x] =
+                Cut{n, unit, (int)blockIdx.x, later == 0 ? 0 : 1 + (int)quotient(later + quantum - 1, quantum)};
+        }
+#pragma unroll
+        for (int u = 0; u < NR; ++u) {
+            const int i = u * BLOCK + tid, r = i / (D / 4), col = (i - r * (D / 4)) * 4;
+            if (r >= rows) break;
+            float big = sm[0][r];
+#pragma unroll
+            for (int v = 1; v < WAVES; ++v) big = fmaxf(big, sm[v][r]);
             const float big0 = big == -INFINITY ? 0.f : big;
             f4 sum = f4(0.f);
             float lsum = 0.f;
 #pragma unroll
-            for (int u = 0; u < WAVES; ++u) {
-                const float f = __builtin_amdgcn_exp2f(sm[u][r] - big0);
-                lsum += f * sl[u][r];
-                sum += f * *reinterpret_cast<const f4 *>(reinterpret_cast<const float *>(lds + u * TL::BYTES) + r * TL::OP + col);
+            for (int v = 0; v < WAVES; ++v) {
+                const float f = __builtin_amdgcn_exp2f(sm[v][r] - big0);
+                lsum += f * sl[v][r];
+                sum += f * *reinterpret_cast<const f4 *>(reinterpret_cast<const float *>(lds + v * TL::BYTES) + r * TL::OP + col);
             }
             if (whole) {
-                finish<T>(d, s.a, n, head0 + r, col, sum, lsum);
+                finish<T>(d, s.a, n, head0 + r, col, sum, inverse_sum(lsum), gate[u]);
             } else {
                 *reinterpret_cast<f4 *>(s.o + (slot * 16 + r) * D + col) = sum;
                 if (col == 0) s.ml[slot * 16 + r] = make_float2(big, lsum);
@@ -351,73 +363,77 @@ __global__ __launch_bounds__(BLOCK, D <= 128 ? 2 : 1) void step_kernel(AttnDims 
     }
 }
 
-// The units that are cut: a block a cut and row.  The first cut of a unit stands for
-// it; the others leave.
-constexpr int JOIN = 512;
+// The units that are cut: a block a unit and 64 quadruples of its rows' channels; each of its waves joins
+// every fourth piece, BATCH at a time.
+constexpr int JOIN = 4, BATCH = 8;
 template <typename T, int D>
-__global__ __launch_bounds__(JOIN) void join_kernel(AttnDims d, StepArgs s)
+__global__ __launch_bounds__(64 * JOIN) void join_kernel(AttnDims d, StepArgs s)
 {
-    constexpr int LANES = D / 4, TEAMS = JOIN / LANES;
-    __shared__ float fac[PARTS_MAX];
-    __shared__ float red[JOIN / 64], sl[JOIN / 64];
-    __shared__ f4 so[TEAMS][LANES];
-    const int64_t b = blockIdx.x + 1;
-    const Place pl = s.place[b];
-    if (pl.n < 0) return;
-    const int64_t pos = b * pl.quantum, local = pos - pl.base;
-    const int nc = chunks_of(d, kv_bound(d, s.a.kv_len, pl.n));
-    const int unit = (int)(local / nc), ch = (int)(local - (int64_t)unit * nc);
-    if (ch == 0 || ch > pl.quantum) return;  // no cut, or not the first one
-    const int kh = unit / s.tiles, head0 = kh * d.g + (unit - kh * s.tiles) * 16, r = blockIdx.y;
-    if (head0 + r >= (kh + 1) * d.g) return;
-    const int parts = 1 + (int)((nc - ch + pl.quantum - 1) / pl.quantum);
-    const int tid = threadIdx.x, team = tid / LANES, lane = tid - team * LANES;
-    // part 0 is the end of block b - 1, the others begin in their block
-    auto slot = [&](int i) { return i == 0 ? 2 * (b - 1) + 1 : 2 * (b - 1 + i); };
+    __shared__ f4 so[JOIN][64];
+    __shared__ float2 sml[JOIN][64];
+    const Cut cut = s.cut[blockIdx.x];
+    if (cut.pieces == 0) return;
+    const int kh = cut.unit / s.tiles, head0 = kh * d.g + (cut.unit - kh * s.tiles) * 16;
+    const int w = scalar(threadIdx.x >> 6), lane = threadIdx.x & 63, i = blockIdx.y * 64 + lane;
+    const int r = i / (D / 4), col = (i - r * (D / 4)) * 4;
+    const bool in = head0 + r < (kh + 1) * d.g;
+    typename Quad<T>::t4 gate = {};
+    if (in && s.a.gate && w == 0) gate = gate_of<T>(d, s.a, cut.n, head0 + r, col);
     float m = -INFINITY, l = 0.f;
-    if (tid < parts) {
-        const float2 x = s.ml[slot(tid) * 16 + r];
-        m = x.x;
-        l = x.y;
+    f4 o = f4(0.f);
+    for (int p0 = w; in && p0 < cut.pieces; p0 += JOIN * BATCH) {
+        float2 ml[BATCH];
+        f4 x[BATCH];
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const int p = p0 + u * JOIN;
+            ml[u] = make_float2(-INFINITY, 0.f);
+            x[u] = f4(0.f);
+            if (p >= cut.pieces) continue;
+            // the first piece is the end of its part, the others begin in theirs
+            const int64_t row = (p == 0 ? 2 * cut.first + 1 : 2 * (cut.first + p)) * 16 + r;
+            ml[u] = s.ml[row];
+            x[u] = *reinterpret_cast<const f4 *>(s.o + row * D + col);
+        }
+        float big = m;
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) big = fmaxf(big, ml[u].x);
+        const float big0 = big == -INFINITY ? 0.f : big, keep = __builtin_amdgcn_exp2f(m - big0);
+        m = big;
+        l *= keep;
+        o *= keep;
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const float f = __builtin_amdgcn_exp2f(ml[u].x - big0);
+            l += f * ml[u].y;
+            o += f * x[u];
+        }
     }
+    so[w][lane] = o;
+    sml[w][lane] = make_float2(m, l);
+    __syncthreads();
+    if (w != 0 || !in) return;
     float big = m;
 #pragma unroll
-    for (int u = 32; u > 0; u >>= 1) big = fmaxf(big, __shfl_xor(big, u, 64));
-    if ((tid & 63) == 0) red[tid >> 6] = big;
-    __syncthreads();
+    for (int u = 1; u < JOIN; ++u) big = fmaxf(big, sml[u][lane].x);
+    const float big0 = big == -INFINITY ? 0.f : big;
+    l = 0.f;
+    o = f4(0.f);
 #pragma unroll
-    for (int u = 0; u < JOIN / 64; ++u) big = fmaxf(big, red[u]);
-    const float f = __builtin_amdgcn_exp2f(m - (big == -INFINITY ? 0.f : big));
-    if (tid < parts) fac[tid] = f;
-    l *= f;
-#pragma unroll
-    for (int u = 32; u > 0; u >>= 1) l += __shfl_xor(l, u, 64);
-    if ((tid & 63) == 0) sl[tid >> 6] = l;
-    __syncthreads();
-    f4 sum = f4(0.f);
-    if (team < TEAMS) {
-#pragma unroll 4
-        for (int i = team; i < parts; i += TEAMS)
-            sum += fac[i] * *reinterpret_cast<const f4 *>(s.o + (slot(i) * 16 + r) * D + lane * 4);
-        so[team][lane] = sum;
+    for (int u = 0; u < JOIN; ++u) {
+        const float f = __builtin_amdgcn_exp2f(sml[u][lane].x - big0);
+        l += f * sml[u][lane].y;
+        o += f * so[u][lane];
     }
-    __syncthreads();
-    if (team == 0) {
-        l = 0.f;
-#pragma unroll
-        for (int u = 0; u < JOIN / 64; ++u) l += sl[u];
-        sum = f4(0.f);
-#pragma unroll
-        for (int u = 0; u < TEAMS; ++u) sum += so[u][lane];
-        finish<T>(d, s.a, pl.n, head0 + r, lane * 4, sum, l);
-    }
+    finish<T>(d, s.a, cut.n, head0 + r, col, o, inverse_sum(l), gate);
 }
 
 struct Plan {
     int tiles, parts;
-    bool cut;  // a unit may be cut
-    size_t place, ml, o;  // bytes
-    size_t bytes() const { return place + ml + o; }
+    int64_t units;
+    bool may_cut;
+    size_t cut, ml, o;  // bytes
+    size_t bytes() const { return cut + ml + o; }
 };
 
 Plan plan_of(const gdn_attn_shape &s)
@@ -426,12 +442,13 @@ Plan plan_of(const gdn_attn_shape &s)
     Plan p;
     p.tiles = (d.g + 15) / 16;
     const int64_t span = d.window < d.max_kv ? d.window : d.max_kv;
-    const int64_t units = (int64_t)d.n_seq * d.KV * p.tiles, most = units * (span <= CHUNK ? 1 : (span + CHUNK - 1) / CHUNK);
+    p.units = (int64_t)d.n_seq * d.KV * p.tiles;
+    const int64_t most = p.units * (span <= CHUNK ? 1 : (span + CHUNK - 1) / CHUNK);
     p.parts = (int)(most < PARTS_MAX ? most : PARTS_MAX);
-    p.cut = span > CHUNK;
-    p.place = ((size_t)p.parts * sizeof(Place) + 255) / 256 * 256;
-    p.ml = p.cut ? (size_t)p.parts * 32 * sizeof(float2) : 0;
-    p.o = p.cut ? (size_t)p.parts * 32 * d.D * sizeof(float) : 0;
+    p.may_cut = span > CHUNK;
+    p.cut = ((size_t)p.parts * sizeof(Cut) + 255) / 256 * 256;
+    p.ml = p.may_cut ? (size_t)p.parts * 32 * sizeof(float2) : 0;
+    p.o = p.may_cut ? (size_t)p.parts * 32 * d.D * sizeof(float) : 0;
     return p;
 }
 
@@ -439,11 +456,13 @@ template <typename T, int D>
 void launch_step_t(const AttnDims &d, const AttnArgs &a, const Plan &p, hipStream_t st)
 {
     char *ws = static_cast<char *>(a.ws);
-    const StepArgs s{a, p.tiles, reinterpret_cast<Place *>(ws), reinterpret_cast<float2 *>(ws + p.place),
-                     reinterpret_cast<float *>(ws + p.place + p.ml)};
-    hipLaunchKernelGGL((step_kernel<T, D>), dim3(p.parts), dim3(BLOCK), 0, st, d, s);
-    if (p.cut && p.parts > 1)
-        hipLaunchKernelGGL((join_kernel<T, D>), dim3(p.parts - 1, d.g < 16 ? d.g : 16), dim3(JOIN), 0, st, d, s);
+    const bool by_unit = p.units <= p.parts;
+    const StepArgs s{a, p.tiles, by_unit, reinterpret_cast<Cut *>(ws), reinterpret_cast<float2 *>(ws + p.cut),
+                     reinterpret_cast<float *>(ws + p.cut + p.ml)};
+    hipLaunchKernelGGL((step_kernel<T, D>), dim3(p.parts), dim3(64 * Tile<T, D>::WAVES), 0, st, d, s);
+    if (p.may_cut && p.parts > 1)
+        hipLaunchKernelGGL((join_kernel<T, D>), dim3(by_unit ? (int)p.units : p.parts - 1, ((d.g < 16 ? d.g : 16) * (D / 4) + 63) / 64),
+                           dim3(64 * JOIN), 0, st, d, s);
 }
 
 } // namespace

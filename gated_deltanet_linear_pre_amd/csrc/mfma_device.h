@@ -85,7 +85,7 @@ __device__ __forceinline__ void split8(const float (&v)[8], typename Mat<T>::fra
         for (int i = 0; i < 8; ++i) out[p][i] = o[p][i];
 }
 
-// the largest of the four lanes that share lane & 15 (x >= 0): a lane-half
+// the largest of the four lanes that share lane & 15: a lane-half
 // swap of x with itself leaves the two halves' values side by side, and a
 // swap of 16-lane rows likewise
 __device__ __forceinline__ float max_of_groups(float x)
