@@ -56,4 +56,23 @@ __device__ __forceinline__ void finish(const AttnDims &d, const AttnArgs &a, int
 // 1 / sum of weights; no key: o and the sum are 0 (a NaN stays one)
 __device__ __forceinline__ float inverse_sum(float l) { return l > 0.f ? 1.0f / l : l; }
 
+// 16 bytes a lane from memory (base and the lane's offset) to LDS (`to`, lane after lane).  Written in
+// assembly because the compiler does not count it then: it would put a wait for all of them before
+// the next LDS read.  wait_vmem_all() and a barrier stand before the data is read.
+// ONCE: past the caches' order.
+template <bool ONCE = false>
+__device__ __forceinline__ void copy_to_lds(const void *base, unsigned offset, unsigned to)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // (that nobody saves m0 for us: nothing here keeps it)
+    const unsigned at = __builtin_amdgcn_readfirstlane(to);
+    if (ONCE)
+        __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(at), "v"(offset), "s"(base) : "memory", "m0");
+    else
+        __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(offset), "s"(base) : "memory", "m0");
+#pragma clang diagnostic pop
+#endif
+}
+
 } // namespace gdn

@@ -221,21 +221,6 @@ __device__ __forceinline__ typename Mat<T>::frag column(const T *v, int k, int t
     }
 }
 
-// 16 bytes a lane from memory (base and the lane's offset) to LDS (`to`, lane after lane).  Written in
-// assembly because the compiler does not count it then: it would put a wait for all of them before
-// the next LDS read.  wait_vmem_all() and a barrier stand before the data is read.
-__device__ __forceinline__ void copy_to_lds(const void *base, unsigned offset, unsigned to)
-{
-#ifdef __HIP_DEVICE_COMPILE__
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"  // (that nobody saves m0 for us: nothing here keeps it)
-    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(to)),
-                     "v"(offset), "s"(base)
-                     : "memory", "m0");
-#pragma clang diagnostic pop
-#endif
-}
-
 // Keeps an operand's registers from being given away before this point
 template <typename F>
 __device__ __forceinline__ void in_use(const F &f)

@@ -6,7 +6,7 @@
 // a matrix product (a unit: sequence, key-value head, 16 query heads), and K and V
 // are read once: bound by HBM bandwidth.
 //
-// Work.  The keys of all units, in chunks of 64, form one line that is cut into equal
+// Work.  The keys of all units, in chunks of 128, form one line that is cut into equal
 // parts, one a block: every block finds its place by a prefix sum over kv_len, so the
 // parts are equal whatever the lengths are, also in a captured call whose lengths
 // have grown.  A block walks the segments (units, or pieces of them) of its part.  A
@@ -14,22 +14,22 @@
 // maximum and weights' sum in the workspace (a part cuts two units at most, at its
 // ends), and a second kernel joins them.
 //
-// gfx950 mapping.  256 parts, one a CU (512 parts: 4 us more for their joins and ends), of 8 waves (4
-// of twice the registers where a head is wide) that take tiles of KT keys in turn, each on its own, with no
-// barrier.  S^T = K Q^T puts a key a row and a query a
+// gfx950 mapping.  256 parts, one a CU (512: 3 to 10 us more, for their joins and ends), of 8 waves (4 of
+// twice the registers for fp32 of wide heads) that take tiles of KT keys in turn, each on its own,
+// with no barrier.  S^T = K Q^T puts a key a row and a query a
 // column: the columns' maxima and sums stay in their lanes, and the weights of lane
 // (gq, c) are keys 4 gq + 0..3 of a tile, which is at once the operand of O^T = V^T w
-// if V^T is read in the same order of keys.  K goes from memory to the operands
-// directly; V through LDS, whose transposing reads give 4 keys of a channel a lane.
-// While a tile is computed the next one's K and V are loaded to registers; they are read once, so
-// past the caches' order (83 us with it for what takes 76 without).
+// if V^T is read in the same order of keys.  While a tile is computed the next one's K is loaded to the
+// operands and its V copied to LDS without registers, whose transposing reads give 4 keys of a channel a
+// lane (V through registers, and so 4 waves a CU at D = 256: 88 us for what takes 79).
+// Both are read once, so past the caches' order (83 us without for 76).
 //
 // Precision.  Scores, maxima, sums and O are fp32.  16-bit weights enter the product
 // with V in two parts of the matrix type (2^-16 of a weight at bf16, 2^-22 at fp16, or
 // 2^-25 of the largest): the matrix pipes have the time.
 //
-// Measured: one sequence of 99991 keys, 32 heads of 128 over 8, fp16, 73 us (5.6 TB/s); 64 sequences of up to
-// 20011 keys, 16 heads of 256 over 2, bf16, 88 us (4.7 TB/s); one of 701 keys 11 us.
+// Measured: one sequence of 99991 keys, 32 heads of 128 over 8, fp16, 71 us (5.8 TB/s); 64 sequences of up to
+// 20011 keys, 16 heads of 256 over 2, bf16, 79 us (5.2 TB/s); one of 701 keys 11 us.
 #include "attn_device.h"
 #include "mfma_device.h"
 
@@ -37,8 +37,9 @@ namespace gdn {
 
 namespace {
 
-constexpr int CHUNK = 64;       // keys that a unit is cut at
-constexpr int PARTS_MAX = 256;  // blocks of a launch
+// Keys that a unit is cut at (128: 701 keys 11.7 us for 10.9, 64 ragged sequences 77.7 for 79.3; 32: 85.2) and
+// blocks of a launch
+constexpr int CHUNK = 64, PARTS_MAX = 256;
 
 // A unit that is cut, for the kernel that joins: its sequence and place in it, the part it begins in, and
 // how many parts have a piece (0: it is not cut)
@@ -55,63 +56,99 @@ struct StepArgs {
     float *o;      // [2 parts][16][D]
 };
 
+// Chunks, tiles and the 16 keys of a product begin at multiples of 16, so that each of the latter
+// lies in one page
+__device__ __forceinline__ int first_chunk(const AttnDims &d, int len) { return first_key(d, len - 1) & ~15; }
 __device__ __forceinline__ int chunks_of(const AttnDims &d, int len)
 {
-    const int span = len - first_key(d, len - 1);
+    const int span = len - first_chunk(d, len);
     return span <= CHUNK ? 1 : (span + CHUNK - 1) / CHUNK;
 }
 
 template <typename T, int D> struct Tile {
-    static constexpr int KT = sizeof(T) == 2 ? 32 : 16;  // keys
+    static constexpr int KT = sizeof(T) == 2 && D <= 128 ? 32 : 16;  // keys
     static constexpr int NT = KT / 16, NC = D / 32, ND = D / 16;
-    static constexpr int WAVES = D <= 128 ? 8 : 4;
-    static constexpr int PER_SIMD = D <= 128 ? 2 : 1;  // waves
-    static constexpr int V = Vec16<T>::n;
-    static constexpr int NV = KT * D / V / 64;      // vectors of V a lane
-    static constexpr int PITCH = D + 32 / sizeof(T);  // of V in LDS: 16 rows of 32 bytes then lie in 8 different groups of banks
-    static constexpr int OP = D + 4;                // of O in LDS
-    static constexpr int BYTES = KT * PITCH * sizeof(T) > 16 * OP * 4 ? KT * PITCH * sizeof(T) : 16 * OP * 4;
+    static constexpr int WAVES = D <= 128 || sizeof(T) == 2 ? 8 : 4;
+    static constexpr int PER_SIMD = WAVES == 8 ? 2 : 1;  // waves
+    static constexpr int V = Vec16<T>::n, LINE = D / V;  // values of a vector of 16 bytes, vectors of a row
+    static constexpr int NV = KT * LINE / 64;            // vectors of V a lane moves
+    static constexpr int GV = 16 * LINE / 64;            // of 16 rows
+    static_assert(GV * 64 == 16 * LINE, "16 rows are whole vectors of a wave");
+    // Rows of V lie in LDS without gaps; vector x of a row stands at place x ^ swap of its row, which lets a
+    // read meet every bank once: 16 bits, 2 vectors of 8 rows; fp32, 4 vectors of rows that are 4 apart.
+    // FOLD: rows until the banks repeat.
+    static constexpr int FOLD = LINE % 16 == 0 ? 1 : LINE % 8 == 0 ? 2 : 4;
+    static constexpr int UNIT = sizeof(T) == 4 ? 4 : 2, APART = sizeof(T) == 4 ? 4 : 1;
+    static constexpr int SHIFT = FOLD > APART ? FOLD : APART, KINDS = 16 / UNIT / FOLD > 0 ? 16 / UNIT / FOLD : 1;
+    static __device__ __forceinline__ int swap(int row) { return (row / SHIFT) % KINDS * UNIT; }
+    static_assert(LINE % (KINDS * UNIT) == 0 && 16 % (SHIFT * KINDS) == 0, "within a row, and the same 16 rows further");
+    static constexpr int OP = D + 4;  // of O in LDS
+    static constexpr int BYTES = 2 * KT * D * sizeof(T) > 16 * OP * 4 ? 2 * KT * D * sizeof(T) : 16 * OP * 4;
 };
 
-// 16 keys x 16 queries, or 16 channels x 16 queries
+// o += V^T w of a tile, its weights in two parts.  KT = 16 takes products of half the depth.
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef short s8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ f4 mma16(_Float16 __attribute__((ext_vector_type(4))) a, _Float16 __attribute__((ext_vector_type(4))) b, f4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f4 mma16(bf16 __attribute__((ext_vector_type(4))) a, bf16 __attribute__((ext_vector_type(4))) b, f4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s4, a), __builtin_bit_cast(s4, b), c, 0, 0, 0);
+}
 template <typename T, int D>
 __device__ __forceinline__ void weigh(const T *v, const float *w, int lane, f4 (&o)[D / 16])
 {
     typedef Mat<T> MT;
-    constexpr int PITCH = Tile<T, D>::PITCH;
-    typename MT::frag p[2];
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = w[i];
-    split8<T, 2>(x, p);
-    const int gq = lane >> 4, c = lane & 15;
-    typedef short s4 __attribute__((ext_vector_type(4)));
-    typedef short s8 __attribute__((ext_vector_type(8)));
+    typedef T t4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s4 lds_s4;
-    const T *at = v + (4 * gq + (c >> 2)) * PITCH + 4 * (c & 3);
-    typename MT::frag f[D / 16];
+    const int row = 4 * (lane >> 4) + ((lane & 15) >> 2), ch = 4 * (lane & 3);
+    const T *rows = v + row * D + ch % 8;
+    auto at = [&](int t) { return rows + (((16 * t + ch) / 8) ^ Tile<T, D>::swap(row)) * 8; };
+    if constexpr (Tile<T, D>::NT == 2) {
+        typename MT::frag p[2], f[D / 16];
+        float x[8];
 #pragma unroll
-    for (int t = 0; t < D / 16; ++t) {
-        const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(at + 16 * t));
-        const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(at + 16 * PITCH + 16 * t));
-        f[t] = __builtin_bit_cast(typename MT::frag, (s8)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+        for (int i = 0; i < 8; ++i) x[i] = w[i];
+        split8<T, 2>(x, p);
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) {
+            const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)at(t));
+            const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(at(t) + 16 * D));
+            f[t] = __builtin_bit_cast(typename MT::frag, (s8)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+        __builtin_amdgcn_sched_barrier(0);  // no load is given registers of an operand in use
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) o[t] = MT::mma(f[t], p[i], o[t]);
+    } else {
+        T part[2][4];
+        t4 p[2], f[D / 16];
+        split<T, 2, 4>(w, part);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i / 4][i % 4] = part[i / 4][i % 4];
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t)
+            f[t] = __builtin_bit_cast(t4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)at(t)));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) o[t] = mma16(f[t], p[i], o[t]);
     }
-    __builtin_amdgcn_sched_barrier(0);  // no load is given registers of an operand in use
-#pragma unroll
-    for (int t = 0; t < D / 16; ++t) o[t] = MT::mma(f[t], p[0], o[t]);
-#pragma unroll
-    for (int t = 0; t < D / 16; ++t) o[t] = MT::mma(f[t], p[1], o[t]);
 }
 template <int D>
 __device__ __forceinline__ void weigh(const float *v, const float *w, int lane, f4 (&o)[D / 16])
 {
-    constexpr int PITCH = Tile<float, D>::PITCH;
-    const float *at = v + 4 * (lane >> 4) * PITCH + (lane & 15);
+    const int row = 4 * (lane >> 4), ch = lane & 15;  // (four rows share their places)
+    const float *rows = v + row * D + ch % 4;
     float f[D / 16][4];
 #pragma unroll
     for (int t = 0; t < D / 16; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[t][i] = at[i * PITCH + 16 * t];
+        for (int i = 0; i < 4; ++i) f[t][i] = rows[i * D + (((16 * t + ch) / 4) ^ Tile<float, D>::swap(row)) * 4];
     __builtin_amdgcn_sched_barrier(0);  // no load is given registers of an operand in use
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -140,7 +177,7 @@ __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) v
     typedef Tile<T, D> TL;
     typedef typename Vec16<T>::type vec;
     constexpr int KT = TL::KT, NT = TL::NT, NC = TL::NC, ND = TL::ND, NV = TL::NV, V = TL::V;
-    __shared__ __attribute__((aligned(16))) char lds[WAVES * TL::BYTES];
+    __shared__ __attribute__((aligned(1024))) char lds[WAVES * TL::BYTES];
     __shared__ float sm[WAVES][16], sl[WAVES][16];
     __shared__ int64_t s_wave[WAVES], s_base;
     __shared__ int s_n;
@@ -191,10 +228,11 @@ __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) v
 
     T *sv = reinterpret_cast<T *>(lds + w * TL::BYTES);
     float *so = reinterpret_cast<float *>(lds + w * TL::BYTES);
+    const unsigned lds_v = (unsigned)(uintptr_t)(__attribute__((address_space(3))) void *)sv;
     const float cs = d.scale * 1.44269504f;
 
     while (pos < stop) {
-        const int len = kv_bound(d, s.a.kv_len, n), first = first_key(d, len - 1), nc = chunks_of(d, len);
+        const int len = kv_bound(d, s.a.kv_len, n), low = first_key(d, len - 1), nc = chunks_of(d, len);
         const int64_t local = pos - base;
         if (local >= (int64_t)nc * units) {
             base += (int64_t)nc * units;
@@ -205,7 +243,7 @@ __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) v
         const int count = stop - pos < nc - ch ? (int)(stop - pos) : nc - ch;
         const int kh = unit / s.tiles, head0 = kh * d.g + (unit - kh * s.tiles) * 16;
         const int rows = (kh + 1) * d.g - head0 < 16 ? (kh + 1) * d.g - head0 : 16;
-        const int begin = first + ch * CHUNK;
+        const int begin = first_chunk(d, len) + ch * CHUNK;
         const int end = ch + count < nc ? begin + count * CHUNK : len;
 
         // ---- queries: column c of the products ----
@@ -234,45 +272,54 @@ __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) v
         float m = -INFINITY, l = 0.f;
 
         const int32_t *table = s.a.table + (int64_t)n * d.table_pages;
-        const T *K = static_cast<const T *>(s.a.k_cache), *Vc = static_cast<const T *>(s.a.v_cache);
+        const int64_t head_at = (int64_t)kh * d.page * D;
+        const T *K = static_cast<const T *>(s.a.k_cache) + head_at, *Vc = static_cast<const T *>(s.a.v_cache) + head_at;
         frag kf[NT][NC];
-        vec vv[NV];
-        // a lane's key of a tile (behind the end: the last one), and its row in the cache
-        auto page_of = [&](int k0) {
-            const int key = k0 + (lane & (KT - 1));
-            return table[(key < end ? key : end - 1) >> d.log_page];
+        // lane t < NT: the page of keys k0 + 16 t.. (behind the end: of the last one), and where they lie
+        const int mine = 16 * (lane & (NT - 1));
+        int page = 0;
+        auto ask = [&](int k0) {
+            const int key = k0 + mine;
+            page = table[(unsigned)(key < end ? key : end - 1) >> d.log_page];
         };
-        auto load = [&](int k0, int page) {
-            int key = k0 + (lane & (KT - 1));
-            key = key < end ? key : end - 1;
-            const int64_t at = cache_row(d, page_bound(d, page), kh, key & (d.page - 1));
+        auto load = [&](int k0, int buf) {
+            const int64_t at = page_bound(d, page) * d.page_stride + ((k0 + mine) & (d.page - 1)) * D;
+            int64_t from[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                from[t] = (uint64_t)(unsigned)__builtin_amdgcn_readlane((int)(at >> 32), t) << 32 | (unsigned)__builtin_amdgcn_readlane((int)at, t);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int t = i / TL::GV, x = i * 64 + lane, r = x / TL::LINE;
+                copy_to_lds<true>(Vc + from[t], (unsigned)(((r - 16 * t) * D + ((x - r * TL::LINE) ^ TL::swap(r)) * V) * sizeof(T)),
+                            lds_v + buf * (int)(KT * D * sizeof(T)) + i * 1024);
+            }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const T *p = K + __shfl((long long)at, 16 * t + c, 64) + 8 * gq;
+                const T *p = K + from[t];
 #pragma unroll
-                for (int i = 0; i < NC; ++i) kf[t][i] = __builtin_nontemporal_load(reinterpret_cast<const typename Frag16<T>::type *>(p + 32 * i));
-            }
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int x = i * 64 + lane, r = x / (D / V);
-                vv[i] = __builtin_nontemporal_load(reinterpret_cast<const vec *>(Vc + __shfl((long long)at, r, 64) + (x - r * (D / V)) * V));
+                for (int i = 0; i < NC; ++i)
+                    kf[t][i] = __builtin_nontemporal_load(reinterpret_cast<const typename Frag16<T>::type *>(p + (unsigned)(c * D + 8 * gq) + 32 * i));
             }
         };
-        int k0 = begin + w * KT;
+        int k0 = begin + w * KT, buf = 0;
         constexpr int STEP = WAVES * KT;
-        int page = 0;
         if (k0 < end) {
-            load(k0, page_of(k0));
-            if (k0 + STEP < end) page = page_of(k0 + STEP);
+            ask(k0);
+            load(k0, 0);
+            ask(k0 + STEP);
         }
-        for (; k0 < end; k0 += STEP) {
-            const bool tail = k0 + KT > end;
-            // V to LDS: rows behind the end as zeros, whatever the cache holds
+        for (; k0 < end; k0 += STEP, buf ^= 1) {
+            wait_vmem_all();  // this tile's V has come
+            __asm__ volatile("" ::: "memory");
+            T *v = sv + buf * (KT * D);
+            const bool cut = k0 + KT > end || k0 < low;
+            if (cut) {  // V of keys that are not seen as zeros, whatever the cache holds
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int x = i * 64 + lane, r = x / (D / V);
-                if (tail && k0 + r >= end) vv[i] = vec(0);
-                st16(sv + r * TL::PITCH + (x - r * (D / V)) * V, vv[i]);
+                for (int i = 0; i < NV; ++i) {
+                    const int x = i * 64 + lane, key = k0 + x / TL::LINE;
+                    if (key < low || key >= end) st16(v + x * V, vec(0));
+                }
             }
             f4 sc[NT];
 #pragma unroll
@@ -281,11 +328,14 @@ __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) v
 #pragma unroll
                 for (int i = 0; i < NC; ++i) sc[t] = MT::mma(kf[t][i], qf[i], sc[t]);
             }
-            if (tail) {
+            if (cut) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[t][i] = k0 + 16 * t + 4 * gq + i < end ? sc[t][i] : -INFINITY;
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = k0 + 16 * t + 4 * gq + i;
+                        sc[t][i] = key >= low && key < end ? sc[t][i] : -INFINITY;
+                    }
             }
             float most = -INFINITY;
 #pragma unroll
@@ -296,8 +346,8 @@ __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) v
             // the next tile, once the products that read these registers are through
             __builtin_amdgcn_sched_barrier(0);
             if (k0 + STEP < end) {
-                load(k0 + STEP, page);
-                if (k0 + 2 * STEP < end) page = page_of(k0 + 2 * STEP);
+                load(k0 + STEP, buf ^ 1);
+                ask(k0 + 2 * STEP);
             }
             if (__any(m1 != m)) {
                 const float keep = __builtin_amdgcn_exp2f(m - (m1 == -INFINITY ? 0.f : m1));
@@ -315,8 +365,8 @@ __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) v
                     wt[4 * t + i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i], cs, -m0));
                     l += wt[4 * t + i];
                 }
-            if constexpr (sizeof(T) == 2) weigh<T, D>(sv, wt, lane, o);
-            else weigh<D>(sv, wt, lane, o);
+            if constexpr (sizeof(T) == 2) weigh<T, D>(v, wt, lane, o);
+            else weigh<D>(v, wt, lane, o);
         }
 
         // ---- the waves' sums joined ----
@@ -441,7 +491,7 @@ Plan plan_of(const gdn_attn_shape &s)
     const AttnDims d = attn_dims(s);
     Plan p;
     p.tiles = (d.g + 15) / 16;
-    const int64_t span = d.window < d.max_kv ? d.window : d.max_kv;
+    const int64_t span = (int64_t)d.window + 15 < d.max_kv ? d.window + 15 : d.max_kv;
     p.units = (int64_t)d.n_seq * d.KV * p.tiles;
     const int64_t most = p.units * (span <= CHUNK ? 1 : (span + CHUNK - 1) / CHUNK);
     p.parts = (int)(most < PARTS_MAX ? most : PARTS_MAX);
