@@ -45,16 +45,24 @@ __device__ __forceinline__ typename Quad<T>::t4 gate_of(const AttnDims &d, const
     return *reinterpret_cast<const typename Quad<T>::t4 *>(static_cast<const T *>(a.gate) + row * d.gate_stride + head * d.D + col);
 }
 template <typename T, typename F4>
-__device__ __forceinline__ void finish(const AttnDims &d, const AttnArgs &a, int64_t row, int head, int col, F4 o, float r,
-                                       typename Quad<T>::t4 gate)
+__device__ __forceinline__ typename Quad<T>::t4 finished(const AttnArgs &a, F4 o, float r, typename Quad<T>::t4 gate)
 {
     typename Quad<T>::t4 y;
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = (T)(a.gate ? o[i] * r * __builtin_amdgcn_rcpf(1.0f + exp_fast(-(float)gate[i])) : o[i] * r);
-    *reinterpret_cast<typename Quad<T>::t4 *>(static_cast<T *>(a.out) + (row * d.H + head) * d.D + col) = y;
+    return y;
+}
+template <typename T, typename F4>
+__device__ __forceinline__ void finish(const AttnDims &d, const AttnArgs &a, int64_t row, int head, int col, F4 o, float r,
+                                       typename Quad<T>::t4 gate)
+{
+    *reinterpret_cast<typename Quad<T>::t4 *>(static_cast<T *>(a.out) + (row * d.H + head) * d.D + col) = finished<T>(a, o, r, gate);
 }
 // 1 / sum of weights; no key: o and the sum are 0 (a NaN stays one)
 __device__ __forceinline__ float inverse_sum(float l) { return l > 0.f ? 1.0f / l : l; }
+
+// What this wave's lanes wrote to LDS before is read by its lanes after (LDS takes a wave's accesses in order)
+__device__ __forceinline__ void wave_sync() { __asm__ volatile("" ::: "memory"); }
 
 // 16 bytes a lane from memory (base and the lane's offset) to LDS (`to`, lane after lane).  Written in
 // assembly because the compiler does not count it then: it would put a wait for all of them before

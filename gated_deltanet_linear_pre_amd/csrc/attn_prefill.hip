@@ -603,42 +603,64 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
 
         l = column_sum<G>(l);
         wait_vmem_all();  // (the copy of the tile behind the last one)
-        if (r < used) {
+#pragma unroll
+        for (int t = 0; t < ND; ++t)
+#pragma unroll
+            for (int i = 0; i < NA; ++i) o[t][i] = dead[(t * NA + i) / 32] >> (t * NA + i) % 32 & 1 ? NAN : o[t][i];
+        if (!LINED || whole) {
+            // Rows leave through LDS, and their gates come so: whole lines of memory, not 8 bytes of each (1024 tokens of
+            // 16 heads of 256 46 -> 44 us)
+            lds_sync();  // every wave has read its last tile
+            constexpr int HELD = 2 * KT / W, NO = W * LINE / 64;  // waves whose rows fit in a buffer; vectors a lane moves
+            T *rows = w < HELD ? sk[0] + w * W * D : sv[0] + (w - HELD) * W * D;
+            const int64_t row = b.row + tok, out_at = (row * d.H + head) * D, gate_at = row * d.gate_stride + (int64_t)head * D;
+            auto vector_of = [&](int x) { return rows + (x / LINE * LINE + (x % LINE ^ TL::swap_k(x / LINE))) * V; };
+            auto quad_of = [&](int col) {
+                return reinterpret_cast<typename Quad<T>::t4 *>(rows + (c * LINE + (col / V ^ TL::swap_k(c))) * V + col % V);
+            };
+            const float inv = inverse_sum(l);
+            if (s.a.gate) {
+                vec gate[NO];
+#pragma unroll
+                for (int i = 0; i < NO; ++i) {
+                    const int x = i * 64 + lane;
+                    gate[i] = ld16(static_cast<const T *>(s.a.gate) + __shfl((long long)gate_at, x / LINE, 64) + x % LINE * V);
+                }
+#pragma unroll
+                for (int i = 0; i < NO; ++i) st16(vector_of(i * 64 + lane), gate[i]);
+                wave_sync();
+            }
 #pragma unroll
             for (int t = 0; t < ND; ++t)
 #pragma unroll
-                for (int i = 0; i < NA; ++i) o[t][i] = dead[(t * NA + i) / 32] >> (t * NA + i) % 32 & 1 ? NAN : o[t][i];
-            if (!LINED || whole) {
-                const float inv = inverse_sum(l);
-                typename Quad<T>::t4 gate[ND][UNITS] = {};  // (all asked for before the first store)
-                if (s.a.gate) {
-#pragma unroll
-                    for (int t = 0; t < ND; ++t)
-#pragma unroll
-                        for (int i = 0; i < UNITS; ++i) gate[t][i] = gate_of<T>(d, s.a, b.row + tok, head, W * t + 4 * G * i + 4 * h);
+                for (int i = 0; i < UNITS; ++i) {
+                    const f4 x = {o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
+                    typename Quad<T>::t4 *at = quad_of(W * t + 4 * G * i + 4 * h);
+                    typename Quad<T>::t4 gate = {};
+                    if (s.a.gate) gate = *at;
+                    *at = finished<T>(s.a, x, inv, gate);
                 }
+            wave_sync();
 #pragma unroll
-                for (int t = 0; t < ND; ++t)
-#pragma unroll
-                    for (int i = 0; i < UNITS; ++i) {
-                        const f4 x = {o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
-                        finish<T>(d, s.a, b.row + tok, head, W * t + 4 * G * i + 4 * h, x, inv, gate[t][i]);
-                    }
-            } else {
-                const int64_t piece = 2 * (int64_t)blockIdx.x + (ch == 0);
-                if (h == 0) s.ml[piece * TL::ROWS + r] = make_float2(m, l);
-#pragma unroll
-                for (int t = 0; t < ND; ++t)
-#pragma unroll
-                    for (int i = 0; i < UNITS; ++i) {
-                        const f4 x = {o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
-                        s.o[((piece * TL::WAVES + w) * ND * UNITS + t * UNITS + i) * 64 + lane] = x;  // whole lines
-                    }
+            for (int i = 0; i < NO; ++i) {
+                const int x = i * 64 + lane;
+                const int64_t to = __shfl((long long)out_at, x / LINE, 64) + x % LINE * V;
+                if (W * w + x / LINE < used) st16(static_cast<T *>(s.a.out) + to, ld16(vector_of(x)));
             }
+        } else if (r < used) {
+            const int64_t piece = 2 * (int64_t)blockIdx.x + (ch == 0);
+            if (h == 0) s.ml[piece * TL::ROWS + r] = make_float2(m, l);
+#pragma unroll
+            for (int t = 0; t < ND; ++t)
+#pragma unroll
+                for (int i = 0; i < UNITS; ++i) {
+                    const f4 x = {o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
+                    s.o[((piece * TL::WAVES + w) * ND * UNITS + t * UNITS + i) * 64 + lane] = x;  // whole lines
+                }
         }
         if constexpr (!LINED) return;
         pos += count;
-        lds_sync();  // every wave has read its last tile
+        lds_sync();  // LDS is free for the next rows
     }
 }
 
