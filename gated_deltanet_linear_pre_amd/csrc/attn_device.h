@@ -61,6 +61,25 @@ __device__ __forceinline__ void finish(const AttnDims &d, const AttnArgs &a, int
 // 1 / sum of weights; no key: o and the sum are 0 (a NaN stays one)
 __device__ __forceinline__ float inverse_sum(float l) { return l > 0.f ? 1.0f / l : l; }
 
+// N pieces of a row (maximum and sum of weights, 4 channels of o) put to what is there
+template <int N, typename F4>
+__device__ __forceinline__ void join(const float2 (&ml)[N], const F4 (&x)[N], float &m, float &l, F4 &o)
+{
+    float big = m;
+#pragma unroll
+    for (int u = 0; u < N; ++u) big = fmaxf(big, ml[u].x);
+    const float big0 = big == -INFINITY ? 0.f : big, keep = __builtin_amdgcn_exp2f(m - big0);
+    m = big;
+    l *= keep;
+    o *= keep;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const float f = __builtin_amdgcn_exp2f(ml[u].x - big0);
+        l += f * ml[u].y;
+        o += f * x[u];
+    }
+}
+
 // What this wave's lanes wrote to LDS before is read by its lanes after (LDS takes a wave's accesses in order)
 __device__ __forceinline__ void wave_sync() { __asm__ volatile("" ::: "memory"); }
 

@@ -130,7 +130,7 @@ struct PrefillArgs {
     int slots;         // blocks along the tokens
     int line;          // blocks among which all keys are dealt in equal parts; 0: a block takes its rows' keys
     // of the line's parts
-    struct Place *place;  // [line]
+    struct Cut *cut;      // [slots][key-value heads and parts of their groups]
     float2 *ml;           // [2 line][rows] maximum (of scores times scale log2 e) and sum of weights
     f4 *o;                // [2 line][wave][4 channels of a row, as a lane holds them][lane]
 };
@@ -138,11 +138,10 @@ struct PrefillArgs {
 // Keys that rows are cut at, and the longest line of slots
 constexpr int CHUNK = 128, MOST_SLOTS = 512;
 
-// Where a part of the line begins: rows (-1: the part is empty), their heads, chunk of theirs and
-// chunks in all, chunks of a part
-struct Place {
-    int slot, hy, ch, nc;
-    unsigned quantum;
+// Rows of a slot and the heads hy of it, whose keys are cut: where their tokens begin and how many they are, the
+// part that the keys begin in, and how many parts have a piece (0: they are not cut)
+struct Cut {
+    int row, tokens, first, pieces;
 };
 
 // over the G lanes of a column
@@ -274,6 +273,8 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
             const bool in = locate<KT>(d, s, i, b);
             s_pre[i] = !in ? 0 : b.end - b.begin <= CHUNK ? 1 : (b.end - b.begin + CHUNK - 1) / CHUNK;
             s_seq[i] = in ? b.n : 0;
+            if (!in && blockIdx.x == 0)
+                for (int k = 0; k < heads; ++k) s.cut[i * heads + k].pieces = 0;
             mine += s_pre[i];
         }
         unsigned upto = mine;
@@ -303,7 +304,6 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
         const uint64_t from = (uint64_t)blockIdx.x * quantum;
         pos = from < total ? (unsigned)from : total;
         stop = total - pos < quantum ? total : pos + quantum;
-        if (pos == stop && threadIdx.x == 0) s.place[blockIdx.x].slot = -1;
     } else {
         // the rows with the most keys first; where all blocks are resident at once, those of the second round the
         // other way about, so that a CU gets a long and a short one (2048 tokens 71 -> 59 us)
@@ -329,6 +329,7 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
         const int lane = tid & 63, h = lane / W, c = lane & (W - 1);
         bool whole = true;
         int ch = 0, count = 0;
+        unsigned left_over = 0;  // chunks of these rows that later parts take
         Work b;
         if constexpr (LINED) {
             int lo = 0, hi = s.slots;
@@ -344,7 +345,7 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
             ch = local - hy * nc;
             count = left < nc - ch ? left : nc - ch;
             whole = count == (int)nc;
-            if (pos == blockIdx.x * quantum && tid == 0) s.place[blockIdx.x] = Place{slot, hy, ch, (int)nc, quantum};
+            left_over = nc - ch - count;
         }
         const int kh = scalar(hy / s.parts), head0 = kh * d.g + (hy - kh * s.parts) * s.heads;
         const int g = (kh + 1) * d.g - head0 < s.heads ? (kh + 1) * d.g - head0 : s.heads;
@@ -354,6 +355,8 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
         b.tokens = scalar(b.tokens);
         b.row = scalar((int)b.row);
         b.p0 = scalar(b.p0);
+        if (LINED && ch == 0 && tid == 0)
+            s.cut[slot * heads + hy] = Cut{(int)b.row, b.tokens, (int)blockIdx.x, left_over == 0 ? 0 : 1 + (int)((left_over + quantum - 1) / quantum)};
         const int begin = scalar(b.begin) + ch * CHUNK, rows_end = scalar(b.end);
         const int end = LINED && rows_end - begin > count * CHUNK ? begin + count * CHUNK : rows_end;
 
@@ -664,42 +667,45 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
     }
 }
 
-// The rows that the line is cut in: a block a cut and 1024 values.  The first cut of a row's keys stands
-// for all; the others leave.
+// The rows whose keys the line is cut in: a block such rows and 1024 values, every piece read once, BATCH at a time
+constexpr int BATCH = 8;
 template <typename T, int D>
 __global__ __launch_bounds__(256) void join_kernel(AttnDims d, PrefillArgs s)
 {
     typedef Tile<T, D> TL;
-    constexpr int KT = TL::KT, ROWS = TL::ROWS, W = TL::W, G = TL::G, UNITS = TL::NA / 4;
-    const int64_t part = blockIdx.x + 1;
-    const Place pl = s.place[part];
-    if (pl.slot < 0 || pl.ch == 0 || (unsigned)pl.ch > pl.quantum) return;
-    const int kh = pl.hy / s.parts, head0 = kh * d.g + (pl.hy - kh * s.parts) * s.heads;
+    constexpr int ROWS = TL::ROWS, W = TL::W, G = TL::G, UNITS = TL::NA / 4;
+    const Cut cut = s.cut[blockIdx.x];
+    if (cut.pieces == 0) return;
+    const int hy = blockIdx.x % (d.KV * s.parts);
+    const int kh = hy / s.parts, head0 = kh * d.g + (hy - kh * s.parts) * s.heads;
     const int g = (kh + 1) * d.g - head0 < s.heads ? (kh + 1) * d.g - head0 : s.heads;
-    Work b;
-    if (!locate<KT>(d, s, pl.slot, b)) return;
     const int at = blockIdx.y * 256 + threadIdx.x, lane = at % 64, unit = at / 64 % (D * W / 256), w = at / 64 / (D * W / 256);
     const int r = W * w + lane % W, col = W * (unit / UNITS) + 4 * G * (unit % UNITS) + 4 * (lane / W);
-    if (r >= b.tokens * g) return;
-    const int n = 1 + (int)((pl.nc - pl.ch + (int64_t)pl.quantum - 1) / pl.quantum);
-    // the first piece is the end of part - 1, the others begin in their part
-    auto piece = [&](int u) { return u == 0 ? 2 * (part - 1) + 1 : 2 * (part - 1 + u); };
-    float big = -INFINITY;
-    for (int u = 0; u < n; ++u) big = fmaxf(big, s.ml[piece(u) * ROWS + r].x);
-    const float big0 = big == -INFINITY ? 0.f : big;
-    float l = 0.f;
-    f4 sum = f4(0.f);
-#pragma unroll 4
-    for (int u = 0; u < n; ++u) {
-        const float2 x = s.ml[piece(u) * ROWS + r];
-        const float f = __builtin_amdgcn_exp2f(x.x - big0);
-        l += f * x.y;
-        sum += f * s.o[piece(u) * (ROWS * D / 4) + at];
-    }
+    if (r >= cut.tokens * g) return;
     const int tok = r / g, head = head0 + r - tok * g;
+    const int64_t row = (int64_t)cut.row + tok;
     typename Quad<T>::t4 gate = {};
-    if (s.a.gate) gate = gate_of<T>(d, s.a, b.row + tok, head, col);
-    finish<T>(d, s.a, b.row + tok, head, col, sum, inverse_sum(l), gate);
+    if (s.a.gate) gate = gate_of<T>(d, s.a, row, head, col);
+    float m = -INFINITY, l = 0.f;
+    f4 o = f4(0.f);
+#pragma unroll 1
+    for (int p0 = 0; p0 < cut.pieces; p0 += BATCH) {
+        float2 ml[BATCH];
+        f4 x[BATCH];
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const int p = p0 + u;
+            ml[u] = make_float2(-INFINITY, 0.f);
+            x[u] = f4(0.f);
+            if (p >= cut.pieces) continue;
+            // the first piece is the end of its part, the others begin in theirs
+            const int64_t piece = p == 0 ? 2 * (int64_t)cut.first + 1 : 2 * ((int64_t)cut.first + p);
+            ml[u] = s.ml[piece * ROWS + r];
+            x[u] = s.o[piece * (ROWS * D / 4) + at];
+        }
+        join<BATCH>(ml, x, m, l, o);
+    }
+    finish<T>(d, s.a, row, head, col, o, inverse_sum(l), gate);
 }
 
 // The line costs about 15 us for its join and one more start and end of rows a block; it is taken where the launch
@@ -709,7 +715,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnDims d, PrefillArgs s)
 constexpr int64_t LINE_KEYS = 640;
 struct Plan {
     int heads, parts, tokens, slots, line;
-    size_t place, ml, o;
+    size_t cut, ml, o;
 };
 Plan plan_of(const AttnDims &d, int rows, int on_cu)
 {
@@ -726,7 +732,7 @@ Plan plan_of(const AttnDims &d, int rows, int on_cu)
     const int64_t resident = 256 * on_cu;
     if (blocks < resident && p.slots <= MOST_SLOTS && span * (resident - blocks) > LINE_KEYS * resident)
         p.line = (int)(most < resident ? most : resident);
-    p.place = ((size_t)p.line * sizeof(Place) + 255) / 256 * 256;
+    p.cut = p.line ? ((size_t)blocks * sizeof(Cut) + 255) / 256 * 256 : 0;
     p.ml = (size_t)p.line * 2 * rows * sizeof(float2);
     p.o = (size_t)p.line * 2 * rows * d.D * sizeof(float);
     return p;
@@ -738,12 +744,12 @@ void launch_prefill_t(const AttnDims &d, const AttnArgs &a, hipStream_t st)
     typedef Tile<T, D> TL;
     const Plan p = plan_of(d, TL::ROWS, TL::BLOCKS);
     char *ws = static_cast<char *>(a.ws);
-    const PrefillArgs s{a, p.heads, p.parts, p.tokens, p.slots, p.line, reinterpret_cast<Place *>(ws),
-                        reinterpret_cast<float2 *>(ws + p.place), reinterpret_cast<f4 *>(ws + p.place + p.ml)};
+    const PrefillArgs s{a, p.heads, p.parts, p.tokens, p.slots, p.line, reinterpret_cast<Cut *>(ws),
+                        reinterpret_cast<float2 *>(ws + p.cut), reinterpret_cast<f4 *>(ws + p.cut + p.ml)};
     const int gy = p.slots < 32768 ? p.slots : 32768;
     const dim3 grid = p.line ? dim3(p.line) : dim3(d.KV * p.parts, gy, (p.slots + gy - 1) / gy);
     hipLaunchKernelGGL((p.line ? prefill_kernel<T, D, true> : prefill_kernel<T, D, false>), grid, dim3(TL::BLOCK), 0, st, d, s);
-    if (p.line > 1) hipLaunchKernelGGL((join_kernel<T, D>), dim3(p.line - 1, TL::ROWS * (D / 4) / 256), dim3(256), 0, st, d, s);
+    if (p.line > 1) hipLaunchKernelGGL((join_kernel<T, D>), dim3(p.slots * d.KV * p.parts, TL::ROWS * (D / 4) / 256), dim3(256), 0, st, d, s);
 }
 
 #define GDN_ATTN_D(...)                                    \
@@ -762,7 +768,7 @@ size_t attn_prefill_workspace_bytes(const gdn_attn_shape &s)
     int rows = 0, blocks = 0;
     GDN_SSM_IO(s.io_dtype, GDN_ATTN_D(rows = Tile<TI, D>::ROWS; blocks = Tile<TI, D>::BLOCKS;))
     const Plan p = plan_of(attn_dims(s), rows, blocks);
-    return p.place + p.ml + p.o;
+    return p.cut + p.ml + p.o;
 }
 
 hipError_t launch_attn_prefill(const gdn_attn_shape &s, const AttnArgs &a, hipStream_t st)

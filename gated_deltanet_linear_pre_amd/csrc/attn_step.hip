@@ -445,19 +445,7 @@ __global__ __launch_bounds__(64 * JOIN) void join_kernel(AttnDims d, StepArgs s)
             ml[u] = s.ml[row];
             x[u] = *reinterpret_cast<const f4 *>(s.o + row * D + col);
         }
-        float big = m;
-#pragma unroll
-        for (int u = 0; u < BATCH; ++u) big = fmaxf(big, ml[u].x);
-        const float big0 = big == -INFINITY ? 0.f : big, keep = __builtin_amdgcn_exp2f(m - big0);
-        m = big;
-        l *= keep;
-        o *= keep;
-#pragma unroll
-        for (int u = 0; u < BATCH; ++u) {
-            const float f = __builtin_amdgcn_exp2f(ml[u].x - big0);
-            l += f * ml[u].y;
-            o += f * x[u];
-        }
+        join<BATCH>(ml, x, m, l, o);
     }
     so[w][lane] = o;
     sml[w][lane] = make_float2(m, l);
