@@ -38,7 +38,7 @@
 //
 // Measured: 2048 tokens of 32 heads of 128, fp16, 53 us (650 TFLOP/s of what the mask leaves), 8192
 // tokens 0.60 ms (912); 8192 tokens of 16 heads of 256, bf16, 0.62 ms (882); chunks of
-// 391 tokens over caches of up to 32768 keys 223 us (712).
+// 391 tokens over caches of up to 32768 keys 219 us (725).
 #include "attn_device.h"
 #include "mfma_device.h"
 
@@ -708,11 +708,16 @@ __global__ __launch_bounds__(256) void join_kernel(AttnDims d, PrefillArgs s)
     finish<T>(d, s.a, row, head, col, o, inverse_sum(l), gate);
 }
 
-// The line costs about 15 us for its join and one more start and end of rows a block; it is taken where the launch
-// would have fewer blocks than are resident at once, and the keys that the idle ones could take are more
-// than LINE_KEYS for each: 64 tokens after 1000 23 us with it and 45 without; 900 from their start 48 and 42; 1024 tokens
-// of 32 heads of 128 51 and 29.
-constexpr int64_t LINE_KEYS = 640;
+// Whether the line is taken, in keys of one block.  Without it the longest rows' keys are the launch's time; with
+// it their average, dealt to all blocks that are resident at once, and what ends and the join
+// cost: more the more parts there are, and the more of them hold ends of two rows.  Measured without and with it:
+// 16 heads of 256, 64 tokens after 1000 45 and 19 us, 300 after 300 31 and 22, 600 from their start 31 and 27,
+// 900 40 and 42, 1500 60 and 84; 32 heads of 128, 512 tokens 20 and 24, after 1500 49 and 42, 1024 30 and 48.
+bool line_pays(double span, double most_new, double line, double blocks, double resident)
+{
+    const double full = blocks / resident, held = span - (most_new < span ? most_new : span) / 2;
+    return span - held * full > 200 * (1 + line / resident + full) + 2000 * full * full;
+}
 struct Plan {
     int heads, parts, tokens, slots, line;
     size_t cut, ml, o;
@@ -728,10 +733,9 @@ Plan plan_of(const AttnDims &d, int rows, int on_cu)
     int64_t span = d.max_kv;
     if (d.window < span && (int64_t)d.window + p.tokens + 64 < span) span = (int64_t)d.window + p.tokens + 64;
     const int64_t most = blocks * ((span + CHUNK - 1) / CHUNK + 1);
-    p.line = 0;
-    const int64_t resident = 256 * on_cu;
-    if (blocks < resident && p.slots <= MOST_SLOTS && span * (resident - blocks) > LINE_KEYS * resident)
-        p.line = (int)(most < resident ? most : resident);
+    const int64_t resident = 256 * on_cu, line = most < resident ? most : resident;
+    const bool few = blocks < resident && p.slots <= MOST_SLOTS;
+    p.line = few && line_pays((double)span, (double)d.max_T, (double)line, (double)blocks, (double)resident) ? (int)line : 0;
     p.cut = p.line ? ((size_t)blocks * sizeof(Cut) + 255) / 256 * 256 : 0;
     p.ml = (size_t)p.line * 2 * rows * sizeof(float2);
     p.o = (size_t)p.line * 2 * rows * d.D * sizeof(float);
