@@ -2,9 +2,11 @@
 //
 //   o = sum_j w_j V_j / sum_j w_j,  w_j = exp(scale q.K_j - max)   over the keys the token sees
 //
-// The g query heads of a key-value head share its keys, so they are the 16 columns of
-// a matrix product (a unit: sequence, key-value head, 16 query heads), and K and V
-// are read once: bound by HBM bandwidth.
+// The g query heads of a key-value head share its keys: 16 are the columns of a matrix
+// product, and up to 8 waves of a block take as many such tiles over the same keys (a unit:
+// sequence, key-value head, those tiles), so that K and V come from memory once: bound by HBM
+// bandwidth.  (Tile after tile, 32 sequences of 8000 keys of 64 heads of 128 over one take 90 us, side by
+// side 54; 16 of 64 heads of 256 over two 90 and 70.)
 //
 // Work.  The keys of all units, in chunks of 128, form one line that is cut into equal
 // parts, one a block: every block finds its place by a prefix sum over kv_len, so the
@@ -22,7 +24,8 @@
 // if V^T is read in the same order of keys.  While a tile is computed the next one's K is loaded to the
 // operands and its V copied to LDS without registers, whose transposing reads give 4 keys of a channel a
 // lane (V through registers, and so 4 waves a CU at D = 256: 88 us for what takes 79).
-// Both are read once, so past the caches' order (83 us without for 76).
+// Both are read once, so past the caches' order (83 us without for 76); not where several waves want the same
+// keys (54 us above, 73 so).
 //
 // Precision.  Scores, maxima, sums and O are fp32.  16-bit weights enter the product
 // with V in two parts of the matrix type (2^-16 of a weight at bf16, 2^-22 at fp16, or
@@ -40,6 +43,7 @@ namespace {
 // Keys that a unit is cut at (128: 701 keys 11.7 us for 10.9, 64 ragged sequences 77.7 for 79.3; 32: 85.2) and
 // blocks of a launch
 constexpr int CHUNK = 64, PARTS_MAX = 256;
+constexpr int waves_of(bool f32, int D) { return f32 && D > 128 ? 4 : 8; }
 
 // A unit that is cut, for the kernel that joins: its sequence and place in it, the part it begins in, and
 // how many parts have a piece (0: it is not cut)
@@ -49,11 +53,12 @@ struct Cut {
 
 struct StepArgs {
     AttnArgs a;
-    int tiles;     // of 16 query heads in a key-value head
+    int wide, log_wide;  // tiles of 16 query heads of a unit: 1, 2, 4 or 8, no more than waves
+    int groups;          // units of a key-value head
     bool by_unit;  // there are no more units than parts: cuts are listed by unit, else by the part they begin in
     Cut *cut;      // [parts]
-    float2 *ml;    // [2 parts][16] maximum (of scores times scale log2 e) and sum of weights
-    float *o;      // [2 parts][16][D]
+    float2 *ml;    // [2 parts][16 wide] maximum (of scores times scale log2 e) and sum of weights
+    float *o;      // [2 parts][16 wide][D]
 };
 
 // Chunks, tiles and the 16 keys of a product begin at multiples of 16, so that each of the latter
@@ -68,7 +73,7 @@ __device__ __forceinline__ int chunks_of(const AttnDims &d, int len)
 template <typename T, int D> struct Tile {
     static constexpr int KT = sizeof(T) == 2 && D <= 128 ? 32 : 16;  // keys
     static constexpr int NT = KT / 16, NC = D / 32, ND = D / 16;
-    static constexpr int WAVES = D <= 128 || sizeof(T) == 2 ? 8 : 4;
+    static constexpr int WAVES = waves_of(sizeof(T) == 4, D);
     static constexpr int PER_SIMD = WAVES == 8 ? 2 : 1;  // waves
     static constexpr int V = Vec16<T>::n, LINE = D / V;  // values of a vector of 16 bytes, vectors of a row
     static constexpr int NV = KT * LINE / 64;            // vectors of V a lane moves
@@ -168,7 +173,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
     return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool WIDE>
 __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) void step_kernel(AttnDims d, StepArgs s)
 {
     constexpr int WAVES = Tile<T, D>::WAVES, BLOCK = 64 * WAVES;
@@ -183,7 +188,10 @@ __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) v
     __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 63, gq = lane >> 4, c = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int units = d.KV * s.tiles;  // of a sequence
+    const int units = d.KV * s.groups;  // of a sequence
+    // the wave's tile of query heads, and its place among the waves that have it
+    const int wide = WIDE ? s.wide : 1, log_wide = WIDE ? s.log_wide : 0;
+    const int qt = w & (wide - 1), team = w >> log_wide, teams = WAVES >> log_wide;
 
     // ---- this block's part of the chunks ----
     const int per = (d.n_seq + BLOCK - 1) / BLOCK;
@@ -224,7 +232,7 @@ __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) v
     }
     __syncthreads();
     int64_t base = s_base;
-    int n = __builtin_amdgcn_readfirstlane(s_n);
+    int n = scalar(s_n);
 
     T *sv = reinterpret_cast<T *>(lds + w * TL::BYTES);
     float *so = reinterpret_cast<float *>(lds + w * TL::BYTES);
@@ -241,8 +249,8 @@ __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) v
         }
         const int unit = (int)quotient(local, nc), ch = (int)(local - (int64_t)unit * nc);
         const int count = stop - pos < nc - ch ? (int)(stop - pos) : nc - ch;
-        const int kh = unit / s.tiles, head0 = kh * d.g + (unit - kh * s.tiles) * 16;
-        const int rows = (kh + 1) * d.g - head0 < 16 ? (kh + 1) * d.g - head0 : 16;
+        const int kh = unit / s.groups, head0 = kh * d.g + (unit - kh * s.groups) * 16 * wide;
+        const int rows = (kh + 1) * d.g - head0 < 16 * wide ? (kh + 1) * d.g - head0 : 16 * wide;
         const int begin = first_chunk(d, len) + ch * CHUNK;
         const int end = ch + count < nc ? begin + count * CHUNK : len;
 
@@ -251,21 +259,23 @@ __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) v
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             qf[i] = frag(0);
-            if (c < rows) {
-                const T *p = static_cast<const T *>(s.a.q) + (int64_t)n * d.q_stride + (int64_t)(head0 + c) * D + 32 * i + 8 * gq;
+            if (16 * qt + c < rows) {
+                const T *p = static_cast<const T *>(s.a.q) + (int64_t)n * d.q_stride + (int64_t)(head0 + 16 * qt + c) * D + 32 * i + 8 * gq;
                 qf[i] = *reinterpret_cast<const typename Frag16<T>::type *>(p);
             }
         }
         const bool whole = count == nc;
         constexpr int NR = (16 * (D / 4) + BLOCK - 1) / BLOCK;
         typename Quad<T>::t4 gate[NR] = {};
-        if (whole && s.a.gate) {
+        auto ask_gates = [&](int first, int tid) {  // of 16 rows
+            if (!whole || !s.a.gate) return;
 #pragma unroll
             for (int u = 0; u < NR; ++u) {
                 const int i = u * BLOCK + tid, r = i / (D / 4);
-                if (r < rows) gate[u] = gate_of<T>(d, s.a, n, head0 + r, (i - r * (D / 4)) * 4);
+                if (r < 16 && first + r < rows) gate[u] = gate_of<T>(d, s.a, n, head0 + first + r, (i - r * (D / 4)) * 4);
             }
-        }
+        };
+        ask_gates(0, tid);
         f4 o[ND];
 #pragma unroll
         for (int t = 0; t < ND; ++t) o[t] = f4(0.f);
@@ -282,6 +292,10 @@ __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) v
             const int key = k0 + mine;
             page = table[(unsigned)(key < end ? key : end - 1) >> d.log_page];
         };
+        auto once = [&](const typename Frag16<T>::type *p) -> frag {
+            if constexpr (WIDE) return *p;
+            else return __builtin_nontemporal_load(p);
+        };
         auto load = [&](int k0, int buf) {
             const int64_t at = page_bound(d, page) * d.page_stride + ((k0 + mine) & (d.page - 1)) * D;
             int64_t from[NT];
@@ -291,7 +305,7 @@ __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) v
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int t = i / TL::GV, x = i * 64 + lane, r = x / TL::LINE;
-                copy_to_lds<true>(Vc + from[t], (unsigned)(((r - 16 * t) * D + ((x - r * TL::LINE) ^ TL::swap(r)) * V) * sizeof(T)),
+                copy_to_lds<!WIDE>(Vc + from[t], (unsigned)(((r - 16 * t) * D + ((x - r * TL::LINE) ^ TL::swap(r)) * V) * sizeof(T)),
                             lds_v + buf * (int)(KT * D * sizeof(T)) + i * 1024);
             }
 #pragma unroll
@@ -299,11 +313,11 @@ __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) v
                 const T *p = K + from[t];
 #pragma unroll
                 for (int i = 0; i < NC; ++i)
-                    kf[t][i] = __builtin_nontemporal_load(reinterpret_cast<const typename Frag16<T>::type *>(p + (unsigned)(c * D + 8 * gq) + 32 * i));
+                    kf[t][i] = once(reinterpret_cast<const typename Frag16<T>::type *>(p + (unsigned)(c * D + 8 * gq) + 32 * i));
             }
         };
-        int k0 = begin + w * KT, buf = 0;
-        constexpr int STEP = WAVES * KT;
+        int k0 = 16 * qt < rows ? begin + team * KT : end, buf = 0;
+        const int STEP = teams * KT;
         if (k0 < end) {
             ask(k0);
             load(k0, 0);
@@ -385,27 +399,41 @@ __global__ __launch_bounds__((Tile<T, D>::WAVES * 64), (Tile<T, D>::PER_SIMD)) v
             s.cut[s.by_unit ? n * units + unit : (int)blockIdx.x] =
                 Cut{n, unit, (int)blockIdx.x, later == 0 ? 0 : 1 + (int)quotient(later + quantum - 1, quantum)};
         }
+        int own = tid;
+#ifdef __HIP_DEVICE_COMPILE__
+        if (WIDE) __asm__("" : "+v"(own));  // (what is derived from it would be kept through the tiles)
+#endif
+#pragma unroll 1
+        for (int first = 0; first < (WIDE ? rows : 1); first += 16) {  // the rows of a tile, from the waves that had it
+            if (first > 0) ask_gates(first, own);
 #pragma unroll
-        for (int u = 0; u < NR; ++u) {
-            const int i = u * BLOCK + tid, r = i / (D / 4), col = (i - r * (D / 4)) * 4;
-            if (r >= rows) break;
-            float big = sm[0][r];
+            for (int u = 0; u < NR; ++u) {
+                const int i = u * BLOCK + own, r = i / (D / 4), col = (i - r * (D / 4)) * 4;
+                if (r >= 16 || first + r >= rows) break;
+                float big = -INFINITY, lsum = 0.f;
+                f4 sum = f4(0.f);
+                auto most = [&](int v) { big = fmaxf(big, sm[v][r]); };
+                auto add = [&](int v) {
+                    const float f = __builtin_amdgcn_exp2f(sm[v][r] - (big == -INFINITY ? 0.f : big));
+                    lsum += f * sl[v][r];
+                    sum += f * *reinterpret_cast<const f4 *>(reinterpret_cast<const float *>(lds + v * TL::BYTES) + r * TL::OP + col);
+                };
+                if constexpr (WIDE) {
+                    for (int v = first / 16; v < WAVES; v += wide) most(v);
+                    for (int v = first / 16; v < WAVES; v += wide) add(v);
+                } else {
 #pragma unroll
-            for (int v = 1; v < WAVES; ++v) big = fmaxf(big, sm[v][r]);
-            const float big0 = big == -INFINITY ? 0.f : big;
-            f4 sum = f4(0.f);
-            float lsum = 0.f;
+                    for (int v = 0; v < WAVES; ++v) most(v);
 #pragma unroll
-            for (int v = 0; v < WAVES; ++v) {
-                const float f = __builtin_amdgcn_exp2f(sm[v][r] - big0);
-                lsum += f * sl[v][r];
-                sum += f * *reinterpret_cast<const f4 *>(reinterpret_cast<const float *>(lds + v * TL::BYTES) + r * TL::OP + col);
-            }
-            if (whole) {
-                finish<T>(d, s.a, n, head0 + r, col, sum, inverse_sum(lsum), gate[u]);
-            } else {
-                *reinterpret_cast<f4 *>(s.o + (slot * 16 + r) * D + col) = sum;
-                if (col == 0) s.ml[slot * 16 + r] = make_float2(big, lsum);
+                    for (int v = 0; v < WAVES; ++v) add(v);
+                }
+                if (whole) {
+                    finish<T>(d, s.a, n, head0 + first + r, col, sum, inverse_sum(lsum), gate[u]);
+                } else {
+                    const int64_t row = slot * 16 * wide + first + r;
+                    *reinterpret_cast<f4 *>(s.o + row * D + col) = sum;
+                    if (col == 0) s.ml[row] = make_float2(big, lsum);
+                }
             }
         }
         __syncthreads();  // LDS is free for the next segment
@@ -423,10 +451,10 @@ __global__ __launch_bounds__(64 * JOIN) void join_kernel(AttnDims d, StepArgs s)
     __shared__ float2 sml[JOIN][64];
     const Cut cut = s.cut[blockIdx.x];
     if (cut.pieces == 0) return;
-    const int kh = cut.unit / s.tiles, head0 = kh * d.g + (cut.unit - kh * s.tiles) * 16;
+    const int kh = cut.unit / s.groups, head0 = kh * d.g + (cut.unit - kh * s.groups) * 16 * s.wide;
     const int w = scalar(threadIdx.x >> 6), lane = threadIdx.x & 63, i = blockIdx.y * 64 + lane;
     const int r = i / (D / 4), col = (i - r * (D / 4)) * 4;
-    const bool in = head0 + r < (kh + 1) * d.g;
+    const bool in = r < 16 * s.wide && head0 + r < (kh + 1) * d.g;
     typename Quad<T>::t4 gate = {};
     if (in && s.a.gate && w == 0) gate = gate_of<T>(d, s.a, cut.n, head0 + r, col);
     float m = -INFINITY, l = 0.f;
@@ -441,7 +469,7 @@ __global__ __launch_bounds__(64 * JOIN) void join_kernel(AttnDims d, StepArgs s)
             x[u] = f4(0.f);
             if (p >= cut.pieces) continue;
             // the first piece is the end of its part, the others begin in theirs
-            const int64_t row = (p == 0 ? 2 * cut.first + 1 : 2 * (cut.first + p)) * 16 + r;
+            const int64_t row = (int64_t)(p == 0 ? 2 * cut.first + 1 : 2 * (cut.first + p)) * 16 * s.wide + r;
             ml[u] = s.ml[row];
             x[u] = *reinterpret_cast<const f4 *>(s.o + row * D + col);
         }
@@ -467,7 +495,7 @@ __global__ __launch_bounds__(64 * JOIN) void join_kernel(AttnDims d, StepArgs s)
 }
 
 struct Plan {
-    int tiles, parts;
+    int wide, log_wide, groups, parts;
     int64_t units;
     bool may_cut;
     size_t cut, ml, o;  // bytes
@@ -478,15 +506,17 @@ Plan plan_of(const gdn_attn_shape &s)
 {
     const AttnDims d = attn_dims(s);
     Plan p;
-    p.tiles = (d.g + 15) / 16;
+    const int tiles = (d.g + 15) / 16, waves = waves_of(s.io_dtype == GDN_F32, d.D);
+    for (p.wide = 1, p.log_wide = 0; p.wide < tiles && p.wide < waves; p.wide <<= 1) ++p.log_wide;
+    p.groups = (tiles + p.wide - 1) / p.wide;
     const int64_t span = (int64_t)d.window + 15 < d.max_kv ? d.window + 15 : d.max_kv;
-    p.units = (int64_t)d.n_seq * d.KV * p.tiles;
+    p.units = (int64_t)d.n_seq * d.KV * p.groups;
     const int64_t most = p.units * (span <= CHUNK ? 1 : (span + CHUNK - 1) / CHUNK);
     p.parts = (int)(most < PARTS_MAX ? most : PARTS_MAX);
     p.may_cut = span > CHUNK;
     p.cut = ((size_t)p.parts * sizeof(Cut) + 255) / 256 * 256;
-    p.ml = p.may_cut ? (size_t)p.parts * 32 * sizeof(float2) : 0;
-    p.o = p.may_cut ? (size_t)p.parts * 32 * d.D * sizeof(float) : 0;
+    p.ml = p.may_cut ? (size_t)p.parts * 32 * p.wide * sizeof(float2) : 0;
+    p.o = p.may_cut ? (size_t)p.parts * 32 * p.wide * d.D * sizeof(float) : 0;
     return p;
 }
 
@@ -495,11 +525,11 @@ void launch_step_t(const AttnDims &d, const AttnArgs &a, const Plan &p, hipStrea
 {
     char *ws = static_cast<char *>(a.ws);
     const bool by_unit = p.units <= p.parts;
-    const StepArgs s{a, p.tiles, by_unit, reinterpret_cast<Cut *>(ws), reinterpret_cast<float2 *>(ws + p.cut),
+    const StepArgs s{a, p.wide, p.log_wide, p.groups, by_unit, reinterpret_cast<Cut *>(ws), reinterpret_cast<float2 *>(ws + p.cut),
                      reinterpret_cast<float *>(ws + p.cut + p.ml)};
-    hipLaunchKernelGGL((step_kernel<T, D>), dim3(p.parts), dim3(64 * Tile<T, D>::WAVES), 0, st, d, s);
+    hipLaunchKernelGGL((p.wide > 1 ? step_kernel<T, D, true> : step_kernel<T, D, false>), dim3(p.parts), dim3(64 * Tile<T, D>::WAVES), 0, st, d, s);
     if (p.may_cut && p.parts > 1)
-        hipLaunchKernelGGL((join_kernel<T, D>), dim3(by_unit ? (int)p.units : p.parts - 1, ((d.g < 16 ? d.g : 16) * (D / 4) + 63) / 64),
+        hipLaunchKernelGGL((join_kernel<T, D>), dim3(by_unit ? (int)p.units : p.parts - 1, ((d.g < 16 * p.wide ? d.g : 16 * p.wide) * (D / 4) + 63) / 64),
                            dim3(64 * JOIN), 0, st, d, s);
 }
 

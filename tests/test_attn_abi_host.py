@@ -169,8 +169,8 @@ def test_workspaces_of_the_largest_and_smallest_sizes():
     r = subprocess.run([sys.executable, "-c", QUERY], input=json.dumps(cases), capture_output=True, text=True, cwd=ROOT)
     assert r.returncode == 0, f"the query ended its process: {r.returncode}\n{r.stderr[-500:]}"
     for (H, KV, D, page, n, T, kv, window, io), (a, b) in zip(cases, json.loads(r.stdout)):
-        # at most 512 parts of 128 rows and 256 of 16, twice, and a record for each
-        assert 0 <= a <= 512 * (2 * 128 * (4 * D + 8) + 64) and 256 <= b <= 256 * (2 * 16 * (4 * D + 8) + 64), (H, KV, D, page, n, T, kv, window, io)
+        # at most 512 parts of 128 rows (16 to 128 in a step), twice, and a record for each
+        assert 0 <= a <= 512 * (2 * 128 * (4 * D + 8) + 64) and 256 <= b <= 256 * (2 * (128 if H > 16 * KV else 16) * (4 * D + 8) + 64), (H, KV, D, page, n, T, kv, window, io)
         if T >= 1 << 20:
             assert a == 0  # many rows: nothing is cut
 

@@ -13,7 +13,7 @@ LDS = 160 * 1024  # of a CU
 
 
 @pytest.mark.skipif(not os.path.exists(B.HIPCC), reason="hipcc not installed")
-@pytest.mark.parametrize("src,kernels", [("attn_append.hip", 15), ("attn_copy.hip", 1), ("attn_prefill.hip", 45), ("attn_step.hip", 30)])
+@pytest.mark.parametrize("src,kernels", [("attn_append.hip", 15), ("attn_copy.hip", 1), ("attn_prefill.hip", 45), ("attn_step.hip", 45)])
 def test_no_scratch(src, kernels, tmp_path):
     out = tmp_path / "a.s"
     flags = [f for f in B.CFLAGS if f != "-fPIC"]

@@ -55,6 +55,15 @@ def test_long_caches_with_a_value_that_is_not_finite(gpu, io):
         assert torch.equal(y[:, :, :9], y0[:, :, :9]) and torch.equal(y[:, :, 10:], y0[:, :, 10:])
 
 
+# ------------------------------------------------- many query heads to a key head
+@pytest.mark.parametrize("io", IO)
+@pytest.mark.parametrize("kv,H,KV,D,window", [([3000, 1, 65, 0, 500], 100, 1, 256, 0), ([700, 40], 66, 2, 128, 0), ([1500], 128, 1, 192, 0),
+                                              ([5000, 17], 24, 1, 64, 600), ([900, 901], 160, 2, 96, 33), ([300] * 150, 17, 1, 64, 0)])
+def test_step_of_large_groups(gpu, io, kv, H, KV, D, window):
+    banner("gdn_attn_step large groups", io, kv[:5], H, KV, D, window)
+    Case([1] * len(kv), [n - 1 for n in kv], H, KV, D, 16, io, window=window, stale=float("nan")).run_and_check("step")
+
+
 # --------------------------------------------------------------- many sequences
 @pytest.mark.parametrize("op", ["prefill", "step"])
 def test_many_sequences(gpu, op):
