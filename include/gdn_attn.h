@@ -129,7 +129,9 @@ int gdn_attn_append(const gdn_attn_shape *shape, const int32_t *cu_seqlens, cons
  * is not).  Keys and values that a query does not see, and rows of pages that no
  * token was written to, do not change its output, whatever they hold.  A value that
  * is not finite makes undefined: q its own output row, K those that see it, V those
- * that see it in its channel.
+ * that see it in its channel.  Where few rows meet many keys the keys of all of them are
+ * dealt to the blocks, as in gdn_attn_step: a row's last bits may then depend on the
+ * call's other rows, which say where its keys are cut.  The same call repeats bit for bit.
  * workspace: device scratch of >= gdn_attn_prefill_workspace_bytes(shape)
  * bytes, 256-byte aligned (NULL where that is 0); its contents are undefined
  * after the call, and it must not be shared by calls in flight at the same time.
