@@ -129,6 +129,7 @@ struct PrefillArgs {
     int tokens;        // of a block: rows / heads
     int slots;         // blocks along the tokens
     int line;          // blocks among which all keys are dealt in equal parts; 0: a block takes its rows' keys
+    unsigned worth;    // so many keys fewer in the longest part are worth what it costs; 0: always
     // of the line's parts
     struct Cut *cut;      // [slots][key-value heads and parts of their groups]
     float2 *ml;           // [2 line][rows] maximum (of scores times scale log2 e) and sum of weights
@@ -167,27 +168,27 @@ struct Work {
     int p0;               // its position
     int begin, end;       // keys that the rows see (begin: on a tile)
 };
+// from the sequence, the tokens' first row and number, and the first one's position
 template <int KT>
-__device__ __forceinline__ bool locate(const AttnDims &d, const PrefillArgs &s, int slot, Work &b, int seq = -1)
+__device__ __forceinline__ Work work_of(const AttnDims &d, int n, int row, int tokens, int p0)
+{
+    Work b;
+    b.n = n;
+    b.tokens = tokens;
+    b.row = row;
+    b.p0 = p0;
+    b.end = p0 + tokens > 0 ? p0 + tokens : 0;
+    b.begin = first_key(d, p0) / KT * KT;
+    return b;
+}
+template <int KT>
+__device__ __forceinline__ bool locate(const AttnDims &d, const PrefillArgs &s, int slot, Work &b)
 {
     SeqTile st;
-    if (seq >= 0) {  // known
-        st.n = seq;
-        st.begin = seq_bound(s.a.cu, seq, d.T);
-        st.end = seq_bound(s.a.cu, seq + 1, d.T);
-        st.c = slot - (st.begin / s.tokens + seq);
-    } else if (!find_tile(s.a.cu, d.n_seq, d.T, s.tokens, slot, st)) {
-        return false;
-    }
+    if (!find_tile(s.a.cu, d.n_seq, d.T, s.tokens, slot, st)) return false;
     const int len = st.end - st.begin, first = st.c * s.tokens;
     if (first >= len) return false;
-    b.n = st.n;
-    b.tokens = len - first < s.tokens ? len - first : s.tokens;
-    b.row = st.begin + first;
-    const int kv = kv_bound(d, s.a.kv_len, st.n);
-    b.p0 = kv - len + first;
-    b.end = b.p0 + b.tokens > 0 ? b.p0 + b.tokens : 0;
-    b.begin = first_key(d, b.p0) / KT * KT;
+    b = work_of<KT>(d, st.n, st.begin + first, len - first < s.tokens ? len - first : s.tokens, kv_bound(d, s.a.kv_len, st.n) - len + first);
     return true;
 }
 
@@ -260,34 +261,41 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
     const int heads = d.KV * s.parts;
 
     // ---- this block's rows, or its part of the line ----
-    __shared__ unsigned s_pre[LINED ? MOST_SLOTS + 1 : 1], s_sum[TL::WAVES];
-    __shared__ unsigned short s_seq[LINED ? MOST_SLOTS : 1];  // (less than 2^32 chunks: 512 rows of at most 2^23)
+    __shared__ unsigned s_pre[LINED ? MOST_SLOTS + 1 : 1], s_sum[TL::WAVES], s_most[TL::WAVES];
+    __shared__ int4 s_work[LINED ? MOST_SLOTS : 1];  // a slot's sequence, row, tokens, position
     int slot = 0, hy = 0;
     unsigned pos = 0, stop = 1, quantum = 0;
     if constexpr (LINED) {
         const int tid = threadIdx.x, lane = tid & 63;
         const int per = (s.slots + BLOCK - 1) / BLOCK;
-        unsigned mine = 0;
+        unsigned mine = 0, most = 0;
         for (int i = tid * per; i < s.slots && i < (tid + 1) * per; ++i) {
             Work b;
             const bool in = locate<KT>(d, s, i, b);
             s_pre[i] = !in ? 0 : b.end - b.begin <= CHUNK ? 1 : (b.end - b.begin + CHUNK - 1) / CHUNK;
-            s_seq[i] = in ? b.n : 0;
+            if (in) s_work[i] = make_int4(b.n, (int)b.row, b.tokens, b.p0);
             if (!in && blockIdx.x == 0)
                 for (int k = 0; k < heads; ++k) s.cut[i * heads + k].pieces = 0;
             mine += s_pre[i];
+            most = most > s_pre[i] ? most : s_pre[i];
         }
         unsigned upto = mine;
 #pragma unroll
         for (int u = 1; u < 64; u <<= 1) {
             const unsigned x = __shfl_up(upto, u, 64);
             if (lane >= u) upto += x;
+            const unsigned y = __shfl_xor(most, u, 64);
+            most = most > y ? most : y;
         }
-        if (lane == 63) s_sum[w] = upto;
+        if (lane == 63) {
+            s_sum[w] = upto;
+            s_most[w] = most;
+        }
         __syncthreads();
         unsigned total = 0;
 #pragma unroll
         for (int i = 0; i < TL::WAVES; ++i) {
+            most = most > s_most[i] ? most : s_most[i];
             if (i < w) upto += s_sum[i];
             total += s_sum[i];
         }
@@ -301,9 +309,17 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
         __syncthreads();
         total = __builtin_amdgcn_readfirstlane(total * heads);
         quantum = scalar(total / gridDim.x + (total % gridDim.x != 0));
-        const uint64_t from = (uint64_t)blockIdx.x * quantum;
-        pos = from < total ? (unsigned)from : total;
-        stop = total - pos < quantum ? total : pos + quantum;
+        most = scalar(most);
+        if (s.worth == 0 || (most > quantum && (uint64_t)(most - quantum) * CHUNK > s.worth)) {
+            const uint64_t from = (uint64_t)blockIdx.x * quantum;
+            pos = from < total ? (unsigned)from : total;
+            stop = total - pos < quantum ? total : pos + quantum;
+        } else {  // not worth its cost (there are no more rows than blocks): a block its rows' keys
+            const int i = blockIdx.x / heads, k = blockIdx.x - i * heads;
+            const unsigned here = i < s.slots ? s_pre[i] : 0, nc = i < s.slots ? s_pre[i + 1] - here : 0;
+            pos = scalar(here * heads + k * nc);
+            stop = pos + scalar(nc);
+        }
     } else {
         // the rows with the most keys first; where all blocks are resident at once, those of the second round the
         // other way about, so that a CU gets a long and a short one (2048 tokens 71 -> 59 us)
@@ -349,7 +365,12 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
         }
         const int kh = scalar(hy / s.parts), head0 = kh * d.g + (hy - kh * s.parts) * s.heads;
         const int g = (kh + 1) * d.g - head0 < s.heads ? (kh + 1) * d.g - head0 : s.heads;
-        if (!locate<KT>(d, s, slot, b, LINED ? scalar(s_seq[slot]) : -1)) return;
+        if constexpr (LINED) {
+            const int4 x = s_work[slot];
+            b = work_of<KT>(d, scalar(x.x), scalar(x.y), scalar(x.z), scalar(x.w));
+        } else if (!locate<KT>(d, s, slot, b)) {
+            return;
+        }
         // (the same for all lanes, which a compiler that divides in vector registers does not see)
         b.n = scalar(b.n);
         b.tokens = scalar(b.tokens);
@@ -610,27 +631,34 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
         for (int t = 0; t < ND; ++t)
 #pragma unroll
             for (int i = 0; i < NA; ++i) o[t][i] = dead[(t * NA + i) / 32] >> (t * NA + i) % 32 & 1 ? NAN : o[t][i];
+        // ---- the rows' ends, from the lane anew ----
+        int own = tid;
+#ifdef __HIP_DEVICE_COMPILE__
+        if (LINED) __asm__("" : "+v"(own));  // (as above)
+#endif
+        const int my = own & 63, col0 = 4 * (my / W), mc = my & (W - 1), mr = W * w + mc;
         if (!LINED || whole) {
             // Rows leave through LDS, and their gates come so: whole lines of memory, not 8 bytes of each (1024 tokens of
             // 16 heads of 256 46 -> 44 us)
             lds_sync();  // every wave has read its last tile
             constexpr int HELD = 2 * KT / W, NO = W * LINE / 64;  // waves whose rows fit in a buffer; vectors a lane moves
             T *rows = w < HELD ? sk[0] + w * W * D : sv[0] + (w - HELD) * W * D;
-            const int64_t row = b.row + tok, out_at = (row * d.H + head) * D, gate_at = row * d.gate_stride + (int64_t)head * D;
+            const int mrr = mr < used ? mr : used - 1, mt = mrr / g, head = head0 + mrr - mt * g;
+            const int64_t row = b.row + mt, out_at = (row * d.H + head) * D, gate_at = row * d.gate_stride + (int64_t)head * D;
             auto vector_of = [&](int x) { return rows + (x / LINE * LINE + (x % LINE ^ TL::swap_k(x / LINE))) * V; };
             auto quad_of = [&](int col) {
-                return reinterpret_cast<typename Quad<T>::t4 *>(rows + (c * LINE + (col / V ^ TL::swap_k(c))) * V + col % V);
+                return reinterpret_cast<typename Quad<T>::t4 *>(rows + (mc * LINE + (col / V ^ TL::swap_k(mc))) * V + col % V);
             };
             const float inv = inverse_sum(l);
             if (s.a.gate) {
                 vec gate[NO];
 #pragma unroll
                 for (int i = 0; i < NO; ++i) {
-                    const int x = i * 64 + lane;
+                    const int x = i * 64 + my;
                     gate[i] = ld16(static_cast<const T *>(s.a.gate) + __shfl((long long)gate_at, x / LINE, 64) + x % LINE * V);
                 }
 #pragma unroll
-                for (int i = 0; i < NO; ++i) st16(vector_of(i * 64 + lane), gate[i]);
+                for (int i = 0; i < NO; ++i) st16(vector_of(i * 64 + my), gate[i]);
                 wave_sync();
             }
 #pragma unroll
@@ -638,7 +666,7 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
 #pragma unroll
                 for (int i = 0; i < UNITS; ++i) {
                     const f4 x = {o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
-                    typename Quad<T>::t4 *at = quad_of(W * t + 4 * G * i + 4 * h);
+                    typename Quad<T>::t4 *at = quad_of(W * t + 4 * G * i + col0);
                     typename Quad<T>::t4 gate = {};
                     if (s.a.gate) gate = *at;
                     *at = finished<T>(s.a, x, inv, gate);
@@ -646,19 +674,19 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
             wave_sync();
 #pragma unroll
             for (int i = 0; i < NO; ++i) {
-                const int x = i * 64 + lane;
+                const int x = i * 64 + my;
                 const int64_t to = __shfl((long long)out_at, x / LINE, 64) + x % LINE * V;
                 if (W * w + x / LINE < used) st16(static_cast<T *>(s.a.out) + to, ld16(vector_of(x)));
             }
-        } else if (r < used) {
+        } else if (mr < used) {
             const int64_t piece = 2 * (int64_t)blockIdx.x + (ch == 0);
-            if (h == 0) s.ml[piece * TL::ROWS + r] = make_float2(m, l);
+            if (col0 == 0) s.ml[piece * TL::ROWS + mr] = make_float2(m, l);
 #pragma unroll
             for (int t = 0; t < ND; ++t)
 #pragma unroll
                 for (int i = 0; i < UNITS; ++i) {
                     const f4 x = {o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
-                    s.o[((piece * TL::WAVES + w) * ND * UNITS + t * UNITS + i) * 64 + lane] = x;  // whole lines
+                    s.o[((piece * TL::WAVES + w) * ND * UNITS + t * UNITS + i) * 64 + my] = x;  // whole lines
                 }
         }
         if constexpr (!LINED) return;
@@ -708,21 +736,21 @@ __global__ __launch_bounds__(256) void join_kernel(AttnDims d, PrefillArgs s)
     finish<T>(d, s.a, row, head, col, o, inverse_sum(l), gate);
 }
 
-// Whether the line is taken, in keys of one block.  Without it the longest rows' keys are the launch's time; with
-// it their average, dealt to all blocks that are resident at once, and what ends and the join
-// cost: more the more parts there are, and the more of them hold ends of two rows.  Measured without and with it:
-// 16 heads of 256, 64 tokens after 1000 45 and 19 us, 300 after 300 31 and 22, 600 from their start 31 and 27,
-// 900 40 and 42, 1500 60 and 84; 32 heads of 128, 512 tokens 20 and 24, after 1500 49 and 42, 1024 30 and 48.
-bool line_pays(double span, double most_new, double line, double blocks, double resident)
-{
-    const double full = blocks / resident, held = span - (most_new < span ? most_new : span) / 2;
-    return span - held * full > 200 * (1 + line / resident + full) + 2000 * full * full;
-}
+// What the line costs beside its keys, in us: ends of the parts and the join, more the more parts there are, and
+// the more of them hold ends of two rows.  Measured without and with it: 16 heads of 256, 64 tokens after
+// 1000 45 and 19 us, 300 after 300 31 and 22, 600 from their start 31 and 27, 900 40 and 42, 1500 60 and 84; 32 heads
+// of 128, 512 tokens 20 and 24, after 1500 49 and 42, 1024 30 and 48.  Of batches, 115 tokens after 3780 with five short
+// prompts, 20 heads of 192, 95 and 59; more blocks than are resident, 1475 tokens after 5788, 24 heads of 256, 415 and 307.
+double line_us(double full, double parts) { return 6.6 * (1 + parts + full) + 66 * full * full; }
+// and a key of a block alone on its CU
+double key_us(bool f32, int D) { return f32 ? 0.0006 * D : 0.006 + 0.000105 * D; }
+
 struct Plan {
     int heads, parts, tokens, slots, line;
+    unsigned worth;
     size_t cut, ml, o;
 };
-Plan plan_of(const AttnDims &d, int rows, int on_cu)
+Plan plan_of(const AttnDims &d, bool f32, int rows, int on_cu)
 {
     Plan p;
     p.heads = d.g < rows ? d.g : rows;
@@ -733,9 +761,17 @@ Plan plan_of(const AttnDims &d, int rows, int on_cu)
     int64_t span = d.max_kv;
     if (d.window < span && (int64_t)d.window + p.tokens + 64 < span) span = (int64_t)d.window + p.tokens + 64;
     const int64_t most = blocks * ((span + CHUNK - 1) / CHUNK + 1);
+    // Without the line the longest rows' keys are the launch's time, or two rows' of a block that comes second; with it
+    // the average, dealt to all blocks that are resident at once.  Of a batch only the longest length is known
+    // here: where rows could be short beside it the kernel decides, by the same rule (4 us if it does not).
     const int64_t resident = 256 * on_cu, line = most < resident ? most : resident;
-    const bool few = blocks < resident && p.slots <= MOST_SLOTS;
-    p.line = few && line_pays((double)span, (double)d.max_T, (double)line, (double)blocks, (double)resident) ? (int)line : 0;
+    const double full = (double)blocks / resident, newest = (double)(d.max_T < span ? d.max_T : span), held = span - newest / 2;
+    const double key = key_us(f32, d.D), cost = line_us(full, (double)line / resident) / key;
+    const bool second = blocks > resident;
+    const double alone = second && 2 * (span - newest / full) > span ? 2 * (span - newest / full) : span;
+    const double dealt = held * full / (second ? 1 : d.n_seq);
+    p.line = p.slots <= MOST_SLOTS && blocks <= 2 * resident && most < (int64_t)1 << 31 && alone - dealt > cost + (d.n_seq > 1 ? 4 / key : 0) ? (int)line : 0;
+    p.worth = second ? 0 : 1 + (unsigned)cost;
     p.cut = p.line ? ((size_t)blocks * sizeof(Cut) + 255) / 256 * 256 : 0;
     p.ml = (size_t)p.line * 2 * rows * sizeof(float2);
     p.o = (size_t)p.line * 2 * rows * d.D * sizeof(float);
@@ -746,9 +782,9 @@ template <typename T, int D>
 void launch_prefill_t(const AttnDims &d, const AttnArgs &a, hipStream_t st)
 {
     typedef Tile<T, D> TL;
-    const Plan p = plan_of(d, TL::ROWS, TL::BLOCKS);
+    const Plan p = plan_of(d, sizeof(T) == 4, TL::ROWS, TL::BLOCKS);
     char *ws = static_cast<char *>(a.ws);
-    const PrefillArgs s{a, p.heads, p.parts, p.tokens, p.slots, p.line, reinterpret_cast<Cut *>(ws),
+    const PrefillArgs s{a, p.heads, p.parts, p.tokens, p.slots, p.line, p.worth, reinterpret_cast<Cut *>(ws),
                         reinterpret_cast<float2 *>(ws + p.cut), reinterpret_cast<f4 *>(ws + p.cut + p.ml)};
     const int gy = p.slots < 32768 ? p.slots : 32768;
     const dim3 grid = p.line ? dim3(p.line) : dim3(d.KV * p.parts, gy, (p.slots + gy - 1) / gy);
@@ -771,7 +807,7 @@ size_t attn_prefill_workspace_bytes(const gdn_attn_shape &s)
 {
     int rows = 0, blocks = 0;
     GDN_SSM_IO(s.io_dtype, GDN_ATTN_D(rows = Tile<TI, D>::ROWS; blocks = Tile<TI, D>::BLOCKS;))
-    const Plan p = plan_of(attn_dims(s), rows, blocks);
+    const Plan p = plan_of(attn_dims(s), s.io_dtype == GDN_F32, rows, blocks);
     return p.cut + p.ml + p.o;
 }
 

@@ -39,6 +39,28 @@ def test_chunks_that_go_on_from_long_caches(gpu, io, new, past, H, KV, D, page, 
     assert torch.equal(a[:c.used], c.run("prefill")[:c.used])
 
 
+# rows that may be cut (a workspace is asked for) and are not, or are only by the lengths on the device;
+# more blocks of rows than are resident at once
+MIXED = [
+    ([115, 1, 5, 393, 1, 64], [3780, 0, 0, 37, 0, 2], 20, 2, 192, 64, 0, 3900), ([700], [3000], 24, 4, 256, 64, 0, 3700),
+    ([3, 50], [0, 10], 6, 2, 128, 16, 0, 30000), ([90, 0, 4], [200, 0, 100], 8, 2, 64, 16, 0, 20000), ([650], [900], 32, 8, 256, 16, 700, 1550),
+]
+
+
+@pytest.mark.parametrize("io", IO)
+@pytest.mark.parametrize("new,past,H,KV,D,page,window,max_kv", MIXED, ids=[f"{c[0]}-D{c[4]}" for c in MIXED])
+def test_batches_of_mixed_lengths(gpu, io, new, past, H, KV, D, page, window, max_kv):
+    banner("gdn_attn_prefill mixed", io, new, past, H, KV, D, page, window, max_kv)
+    c = Case(new, past, H, KV, D, page, io, tail=1, window=window, stale=float("nan"))
+    pages = -(-max_kv // page)
+    more = dict(max_kv=max_kv, table_pages=pages)
+    c.table_t = torch.cat([c.table_t, torch.full((c.n, max(0, pages - c.table_t.shape[1])), 1 << 30, dtype=torch.int32, device="cuda")], 1)
+    a = c.run("prefill", **more)
+    c.check("prefill", a)
+    for _ in range(2):
+        assert torch.equal(a[:c.used], c.run("prefill", **more)[:c.used])
+
+
 @pytest.mark.parametrize("io", IO)
 def test_long_caches_with_a_value_that_is_not_finite(gpu, io):
     c = Case([70], [4000], 4, 2, 64, 16, io, gate=False)
