@@ -26,7 +26,7 @@
 // Few rows over many keys (a chunk that goes on from a long cache) would leave most CUs idle.
 // The keys of all rows then form one line that is cut into equal parts, one a block, as in the
 // step: rows within one part are finished there, of rows that are cut each part leaves O, maximum
-// and sum in the workspace, and a second kernel joins them.
+// and sum in the workspace, and a second kernel joins them.  Whether that pays is said by line_us().
 //
 // Precision.  Scores, maxima, sums and O are fp32; 16-bit weights are rounded to the
 // io type for the product with V (half a step of each weight, of random sign: as much as
@@ -36,8 +36,8 @@
 // V that is not finite would turn 0 into NaN there, so it is made 0 in LDS in such
 // a tile, and the rows that see it become NaN in its channel at the end.
 //
-// Measured: 2048 tokens of 32 heads of 128, fp16, 53 us (650 TFLOP/s of what the mask leaves), 8192
-// tokens 0.60 ms (912); 8192 tokens of 16 heads of 256, bf16, 0.62 ms (882); chunks of
+// Measured: 2048 tokens of 32 heads of 128, fp16, 54 us (635 TFLOP/s of what the mask leaves), 8192
+// tokens 0.59 ms (936); 8192 tokens of 16 heads of 256, bf16, 0.62 ms (882); chunks of
 // 391 tokens over caches of up to 32768 keys 219 us (725).
 #include "attn_device.h"
 #include "mfma_device.h"
