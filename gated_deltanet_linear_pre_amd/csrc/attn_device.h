@@ -87,6 +87,9 @@ __device__ __forceinline__ void wave_sync() { __asm__ volatile("" ::: "memory");
 // assembly because the compiler does not count it then: it would put a wait for all of them before
 // the next LDS read.  wait_vmem_all() and a barrier stand before the data is read.
 // ONCE: past the caches' order.
+// The waits that the compiler would put there stand in the assembly too: a load may read a scalar register 5 wait
+// states after a vector instruction (readlane) wrote it, M0 1 after it was written; sooner it could go to the
+// address that the registers held before.  s_mov is one of the 5, s_nop 3 the others.
 template <bool ONCE = false>
 __device__ __forceinline__ void copy_to_lds(const void *base, unsigned offset, unsigned to)
 {
@@ -95,9 +98,9 @@ __device__ __forceinline__ void copy_to_lds(const void *base, unsigned offset, u
 #pragma clang diagnostic ignored "-Winline-asm"  // (that nobody saves m0 for us: nothing here keeps it)
     const unsigned at = __builtin_amdgcn_readfirstlane(to);
     if (ONCE)
-        __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(at), "v"(offset), "s"(base) : "memory", "m0");
+        __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(at), "v"(offset), "s"(base) : "memory", "m0");
     else
-        __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(offset), "s"(base) : "memory", "m0");
+        __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(offset), "s"(base) : "memory", "m0");
 #pragma clang diagnostic pop
 #endif
 }
