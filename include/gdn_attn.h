@@ -142,7 +142,11 @@ int gdn_attn_prefill(const gdn_attn_shape *shape, const int32_t *cu_seqlens, con
                      size_t workspace_bytes, void *stream);
 
 /* Bytes of scratch gdn_attn_prefill needs for `shape` (0 also if the shape is
- * invalid, which gdn_attn_prefill reports). */
+ * invalid, which gdn_attn_prefill reports).  The need is each shape's own: one of fewer
+ * tokens or shorter caches may need more (few rows have their keys dealt, many do not:
+ * with 16 heads of 256 over 2 and max_kv 32768, 1024 tokens need 68 MB and 8192 none).  To allocate once,
+ * take the bound for all shapes of a head_dim and type, 8 P R (head_dim + 2) + 32 P bytes, with P = 512
+ * for head_dim up to 128 and 256 above, R = 128 and for GDN_F32 64. */
 size_t gdn_attn_prefill_workspace_bytes(const gdn_attn_shape *shape);
 
 /*
@@ -159,7 +163,7 @@ int gdn_attn_step(const gdn_attn_shape *shape, const int32_t *kv_len, const int3
                   void *out, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Bytes of scratch gdn_attn_step needs for `shape` (0 also if the shape is
- * invalid). */
+ * invalid).  With the same heads and type it falls with no size but `window` (0 needs the most). */
 size_t gdn_attn_step_workspace_bytes(const gdn_attn_shape *shape);
 
 /*
