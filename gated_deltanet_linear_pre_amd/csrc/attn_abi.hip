@@ -18,6 +18,7 @@ constexpr int64_t kMaxKv = (int64_t)1 << 30;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 constexpr int64_t kMaxCache = (int64_t)1 << 56;  // elements
 constexpr int64_t kMaxPairs = (int64_t)1 << 24;
+constexpr float kMaxScale = 0x1p127f;  // (times log2 e it is still finite: an infinite one would make a score of 0 NaN)
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 int elem(int32_t t) { return t == GDN_F32 ? 4 : 2; }
@@ -58,7 +59,7 @@ int check_shape(const gdn_attn_shape *s)
     if (s->rope_dim < 0 || s->rope_dim > D || s->rope_dim % 16) return GDN_E_SHAPE;
     if (s->flags & ~GDN_ROPE_PAIRS || s->reserved) return GDN_E_SHAPE;
     if (s->window < 0) return GDN_E_SHAPE;
-    if (!(isfinite(s->scale) && s->scale > 0.f)) return GDN_E_SHAPE;
+    if (!(s->scale > 0.f && s->scale <= kMaxScale)) return GDN_E_SHAPE;
     if (!(isfinite(s->rope_scale) && s->rope_scale >= 0.f) || !(isfinite(s->eps) && s->eps >= 0.f)) return GDN_E_SHAPE;
     const int e = elem(s->io_dtype);
     if (s->page_stride * e % 16 || s->q_stride * e % 16 || s->k_stride * e % 16 || s->v_stride * e % 16 ||

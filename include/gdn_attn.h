@@ -74,7 +74,7 @@ extern "C" {
  * total_T <= 2^26; 1 <= n_pages; 1 <= table_pages; 0 <= max_kv <= 2^30 and
  * max_kv <= table_pages * page_size; strides 0 or a row's (page's) elements up
  * to 2^40; n_pages * page_stride <= 2^56; rope_dim a multiple of 16 up to
- * head_dim; window >= 0; scale > 0, rope_scale and eps >= 0, all finite.
+ * head_dim; window >= 0; 0 < scale <= 2^127; rope_scale and eps >= 0, both finite.
  * Every entry point checks all of it, whichever fields it reads. */
 typedef struct gdn_attn_shape {
     int32_t heads, kv_heads, head_dim, page_size;

@@ -47,3 +47,14 @@ def test_a_steps_workspace_grows_with_its_sizes(io, D, H, kv_heads):
             assert needs == sorted(needs)
     for kv in KV:
         assert all(size(3, kv, window) <= size(3, kv, 0) for window in (1, 100, 5000))
+
+
+@pytest.mark.parametrize("scale,code", [(2.0 ** 127, 0), (2.0 ** 127 * (1 + 2.0 ** -23), -2), (2.4e38, -2), (3.4e38, -2), (2.0 ** -149, 0)])
+def test_scales_that_the_kernels_can_form(scale, code):
+    """Scores are formed times scale log2(e), which has to be finite: refused, or (with no rows) not."""
+    s = shape(8, 2, 128, "bf16", 0, 100)
+    s.scale = scale
+    P = 0x10000  # an address that is never used
+    need = attn.gdn_attn_prefill_workspace_bytes(s)
+    assert attn.gdn_attn_prefill(s, P, P, P, P, P, P, None, P, P, workspace_bytes=need, stream=0, check=False) == code
+    assert attn.gdn_attn_append(s, P, P, P, None, P, P, P, None, None, None, P, P, P, stream=0, check=False) == code
