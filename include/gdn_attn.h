@@ -43,7 +43,9 @@
  *   gate    [total_T][H][D]     or NULL (no gate)
  *   out, q_out [total_T][H][D]  dense
  * q, k, v and gate may be column blocks of a wider projection: the strides
- * give the elements between token rows.
+ * give the elements between token rows.  The heads of a row lie side by side: a
+ * projection that leaves q and gate of a head next to each other has its weights'
+ * rows put in order once, when they are loaded.
  * The integers on the device are preconditions, since checking them would take
  * a synchronisation.  No access leaves the buffers whatever they hold: cu_seqlens
  * outside [0, total_T] and kv_len outside [0, max_kv] are taken as the nearer
@@ -109,6 +111,9 @@ typedef struct gdn_attn_shape {
  * rotation in fp32, one rounding to io; the angle is formed in 64 bits, so that it is
  * as exact for a far position as for the first (2^-21 at position 2^30).
  * Tokens at a position p below 0 or not below max_kv are not written to the cache.
+ * No two tokens of a call may fall on one row of a page, or it may hold a mixture
+ * (sequences that share a page which they still write to are forked first,
+ * gdn_attn_copy_pages).
  * inv_freq [rope_dim/2] fp32 (may be NULL with rope_dim 0).
  * In: cu_seqlens, kv_len, page_table, positions, q, k, v, inv_freq, q_norm,
  * k_norm.  Out: q_out; k_cache, v_cache (the written rows only).
@@ -123,13 +128,15 @@ int gdn_attn_append(const gdn_attn_shape *shape, const int32_t *cu_seqlens, cons
  * the keys j with max(0, p - window + 1) <= j <= p (from 0 with window 0):
  *   w_j = exp(scale q[t][h] . K_j - max),  o = sum_j w_j V_j / sum_j w_j
  *   out = o, or o sigmoid(gate[t][h])
- * A query that sees no key (p < 0) gets 0.  The keys of the new tokens are in the
+ * A query that sees no key (p < 0) has o = 0.  The keys of the new tokens are in the
  * cache already (gdn_attn_append).  Scores, maxima, sums and o are fp32; with 16-bit
  * io the weights w_j are rounded to io as operands of the product with V (their sum
  * is not).  Keys and values that a query does not see, and rows of pages that no
  * token was written to, do not change its output, whatever they hold.  A value that
  * is not finite makes undefined: q its own output row, K those that see it, V those
- * that see it in its channel.  Where few rows meet many keys the keys of all of them are
+ * that see it in its channel, gate its own value.  Scores times log2 e, and sums over
+ * the keys of up to 2^8 |V_j|, have to stay inside fp32's range, or the row or the
+ * channel is undefined too.  Where few rows meet many keys the keys of all of them are
  * dealt to the blocks, as in gdn_attn_step: a row's last bits may then depend on the
  * call's other rows, which say where its keys are cut.  The same call repeats bit for bit.
  * workspace: device scratch of >= gdn_attn_prefill_workspace_bytes(shape)
@@ -186,7 +193,9 @@ int gdn_attn_copy_pages(const gdn_attn_shape *shape, const int32_t *pairs, int64
  *   GDN_ROPE_PARTS   by the turns u = trained f_i / (2 pi) of a pair: f_i where u >=
  *                    fast, f_i / factor where u <= slow, in between
  *                    f_i (r + (1 - r) / factor), r = (u - slow) / (fast - slow);
- *                    rope_scale 0.1 ln(factor) + 1
+ *                    rope_scale 0.1 ln(factor) + 1.  The ramp is linear in the turns; a
+ *                    model whose ramp is linear in the pair's index has other frequencies
+ *                    between the two ends, and passes a table of its own
  * rope_scale is 1 for the others. */
 typedef enum gdn_rope_kind {
     GDN_ROPE_PLAIN = 0,
