@@ -83,16 +83,6 @@ template <> struct Mma<_Float16, 32> {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
     }
 };
-// fp32: eight 2-deep products; product i contracts value i of both lane halves
-template <> struct Mma<float, 32> {
-    typedef f16v acc;
-    static __device__ __forceinline__ f16v mma(Mat<float>::frag a, Mat<float>::frag b, f16v c)
-    {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
-        return c;
-    }
-};
 
 template <typename T, int D> struct Tile {
     static constexpr int W = sizeof(T) == 4 || D > 128 ? 16 : 32;  // rows of a wave
