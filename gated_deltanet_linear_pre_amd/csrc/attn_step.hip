@@ -8,7 +8,7 @@
 // bandwidth.  (Tile after tile, 32 sequences of 8000 keys of 64 heads of 128 over one take 90 us, side by
 // side 54; 16 of 64 heads of 256 over two 90 and 70.)
 //
-// Work.  The keys of all units, in chunks of 128, form one line that is cut into equal
+// Work.  The keys of all units, in chunks of 64, form one line that is cut into equal
 // parts, one a block: every block finds its place by a prefix sum over kv_len, so the
 // parts are equal whatever the lengths are, also in a captured call whose lengths
 // have grown.  A block walks the segments (units, or pieces of them) of its part.  A
