@@ -118,6 +118,7 @@ struct PrefillArgs {
     int heads, parts;  // of a key-value head's group that a block takes; parts of the group
     int tokens;        // of a block: rows / heads
     int slots;         // blocks along the tokens
+    bool paired;       // the blocks that have rows are all resident at once
     int line;          // blocks among which all keys are dealt in equal parts; 0: a block takes its rows' keys
     unsigned worth;    // so many keys fewer in the longest part are worth what it costs; 0: always
     // of the line's parts
@@ -312,12 +313,13 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
         }
     } else {
         // the rows with the most keys first; where all blocks are resident at once, those of the second round the
-        // other way about, so that a CU gets a long and a short one (2048 tokens 71 -> 59 us)
+        // other way about, so that a CU gets a long and a short one (2048 tokens of 32 heads of 128 60.5 -> 58.8 us, two
+        // prompts of 1000 42.6 -> 37.0; with more blocks it costs: 2079 tokens after 2000 153 -> 173, 2480 73 -> 79)
         int q = blockIdx.z * gridDim.y + blockIdx.y;
         if (q >= s.slots) return;
         hy = blockIdx.x;
         constexpr int FIRST = 256;
-        if (TL::BLOCKS == 2 && (int64_t)s.slots * heads <= 640) {
+        if (TL::BLOCKS == 2 && s.paired) {
             const int all = s.slots * heads, at = q * heads + hy;
             if (at >= FIRST) {
                 q = scalar((all - 1 - (at - FIRST)) / heads);
@@ -737,6 +739,7 @@ double key_us(bool f32, int D) { return f32 ? 0.0006 * D : 0.006 + 0.000105 * D;
 
 struct Plan {
     int heads, parts, tokens, slots, line;
+    bool paired;
     unsigned worth;
     size_t cut, ml, o;
 };
@@ -755,6 +758,7 @@ Plan plan_of(const AttnDims &d, bool f32, int rows, int on_cu)
     // the average, dealt to all blocks that are resident at once.  Of a batch only the longest length is known
     // here: where rows could be short beside it the kernel decides, by the same rule (4 us if it does not).
     const int64_t resident = 256 * on_cu, line = most < resident ? most : resident;
+    p.paired = ((d.T > d.n_seq ? (d.T - d.n_seq) / p.tokens : 0) + d.n_seq) * d.KV * p.parts <= resident;
     const double full = (double)blocks / resident, newest = (double)(d.max_T < span ? d.max_T : span), held = span - newest / 2;
     const double key = key_us(f32, d.D), cost = line_us(full, (double)line / resident) / key;
     const bool second = blocks > resident;
@@ -774,7 +778,7 @@ void launch_prefill_t(const AttnDims &d, const AttnArgs &a, hipStream_t st)
     typedef Tile<T, D> TL;
     const Plan p = plan_of(d, sizeof(T) == 4, TL::ROWS, TL::BLOCKS);
     char *ws = static_cast<char *>(a.ws);
-    const PrefillArgs s{a, p.heads, p.parts, p.tokens, p.slots, p.line, p.worth, reinterpret_cast<Cut *>(ws),
+    const PrefillArgs s{a, p.heads, p.parts, p.tokens, p.slots, p.paired, p.line, p.worth, reinterpret_cast<Cut *>(ws),
                         reinterpret_cast<float2 *>(ws + p.cut), reinterpret_cast<f4 *>(ws + p.cut + p.ml)};
     const int gy = p.slots < 32768 ? p.slots : 32768;
     const dim3 grid = p.line ? dim3(p.line) : dim3(d.KV * p.parts, gy, (p.slots + gy - 1) / gy);
