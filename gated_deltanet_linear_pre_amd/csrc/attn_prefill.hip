@@ -120,7 +120,7 @@ struct PrefillArgs {
     int slots;         // blocks along the tokens
     bool paired;       // the blocks that have rows are all resident at once
     int line;          // blocks among which all keys are dealt in equal parts; 0: a block takes its rows' keys
-    unsigned worth;    // so many keys fewer in the longest part are worth what it costs; 0: always
+    unsigned worth;    // so many keys fewer in the longest part are worth what it costs
     // of the line's parts
     struct Cut *cut;      // [slots][key-value heads and parts of their groups]
     float2 *ml;           // [2 line][rows] maximum (of scores times scale log2 e) and sum of weights
@@ -256,6 +256,7 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
     __shared__ int4 s_work[LINED ? MOST_SLOTS : 1];  // a slot's sequence, row, tokens, position
     int slot = 0, hy = 0;
     unsigned pos = 0, stop = 1, quantum = 0;
+    __shared__ unsigned s_next[2];  // other rows' keys, which a block takes after these: lower in the line (or none)
     if constexpr (LINED) {
         const int tid = threadIdx.x, lane = tid & 63;
         const int per = (s.slots + BLOCK - 1) / BLOCK;
@@ -300,16 +301,51 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
         __syncthreads();
         total = __builtin_amdgcn_readfirstlane(total * heads);
         quantum = scalar(total / gridDim.x + (total % gridDim.x != 0));
+        // Not dealt, a block takes its rows' keys; where there are more rows than blocks, the last ones first, and the
+        // blocks that have the fewest keys then take second rows.
+        const int blocks = gridDim.x, all = s.slots * heads, extra = all > blocks ? all - blocks : 0;
+        auto first_of = [&](int i) { return extra ? all - 1 - i : i; };
+        auto second_of = [&](int i) { return i - (blocks - extra); };  // (below 0: none)
+        if (extra) {  // the longest of two rows
+            most = 0;
+            for (int i = tid; i < blocks; i += BLOCK) {
+                const int one = first_of(i) / heads, two = second_of(i) / heads;
+                const unsigned n = s_pre[one + 1] - s_pre[one] + (second_of(i) < 0 ? 0 : s_pre[two + 1] - s_pre[two]);
+                most = most > n ? most : n;
+            }
+#pragma unroll
+            for (int u = 1; u < 64; u <<= 1) {
+                const unsigned y = __shfl_xor(most, u, 64);
+                most = most > y ? most : y;
+            }
+            if (lane == 0) s_most[w] = most;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < TL::WAVES; ++i) most = most > s_most[i] ? most : s_most[i];
+        }
         most = scalar(most);
-        if (s.worth == 0 || (most > quantum && (uint64_t)(most - quantum) * CHUNK > s.worth)) {
+        unsigned next = 0, next_stop = 0xffffffff;
+        if (most > quantum && (uint64_t)(most - quantum) * CHUNK > s.worth) {
             const uint64_t from = (uint64_t)blockIdx.x * quantum;
             pos = from < total ? (unsigned)from : total;
             stop = total - pos < quantum ? total : pos + quantum;
-        } else {  // not worth its cost (there are no more rows than blocks): a block its rows' keys
-            const int i = blockIdx.x / heads, k = blockIdx.x - i * heads;
-            const unsigned here = i < s.slots ? s_pre[i] : 0, nc = i < s.slots ? s_pre[i + 1] - here : 0;
-            pos = scalar(here * heads + k * nc);
-            stop = pos + scalar(nc);
+        } else {  // not worth its cost
+            auto take = [&](int row, unsigned &pos, unsigned &stop) {
+                const int i = row / heads, k = row - i * heads;
+                const unsigned here = i < s.slots ? s_pre[i] : 0, nc = i < s.slots ? s_pre[i + 1] - here : 0;
+                pos = scalar(here * heads + k * nc);
+                stop = pos + scalar(nc);
+            };
+            take(first_of(blockIdx.x), pos, stop);
+            if (extra && second_of(blockIdx.x) >= 0) take(second_of(blockIdx.x), next, next_stop);
+            if (pos == stop && next_stop != 0xffffffff) {
+                pos = next;
+                stop = next_stop;
+            }
+        }
+        if (tid == 0) {
+            s_next[0] = next;
+            s_next[1] = next_stop;
         }
     } else {
         // the rows with the most keys first; where all blocks are resident at once, those of the second round the
@@ -684,6 +720,10 @@ __global__ __launch_bounds__((Tile<T, D>::BLOCK), (Tile<T, D>::BLOCKS)) void pre
         if constexpr (!LINED) return;
         pos += count;
         lds_sync();  // LDS is free for the next rows
+        if (pos == stop && (unsigned)scalar(s_next[1]) < stop) {
+            pos = scalar(s_next[0]);
+            stop = scalar(s_next[1]);
+        }
     }
 }
 
@@ -755,8 +795,9 @@ Plan plan_of(const AttnDims &d, bool f32, int rows, int on_cu)
     if (d.window < span && (int64_t)d.window + p.tokens + 64 < span) span = (int64_t)d.window + p.tokens + 64;
     const int64_t most = blocks * ((span + CHUNK - 1) / CHUNK + 1);
     // Without the line the longest rows' keys are the launch's time, or two rows' of a block that comes second; with it
-    // the average, dealt to all blocks that are resident at once.  Of a batch only the longest length is known
-    // here: where rows could be short beside it the kernel decides, by the same rule (4 us if it does not).
+    // the average, dealt to all blocks that are resident at once.  The lengths are not known here but for their
+    // bounds: where the line may pay the kernel decides, by the same rule (4 us if it does not deal; prompts from their
+    // start with max_kv 32768, 16 heads of 256: 2100 tokens 137 -> 87 us, 3500 298 -> 141).
     const int64_t resident = 256 * on_cu, line = most < resident ? most : resident;
     p.paired = ((d.T > d.n_seq ? (d.T - d.n_seq) / p.tokens : 0) + d.n_seq) * d.KV * p.parts <= resident;
     const double full = (double)blocks / resident, newest = (double)(d.max_T < span ? d.max_T : span), held = span - newest / 2;
@@ -765,7 +806,7 @@ Plan plan_of(const AttnDims &d, bool f32, int rows, int on_cu)
     const double alone = second && 2 * (span - newest / full) > span ? 2 * (span - newest / full) : span;
     const double dealt = held * full / (second ? 1 : d.n_seq);
     p.line = p.slots <= MOST_SLOTS && blocks <= 2 * resident && most < (int64_t)1 << 31 && alone - dealt > cost + (d.n_seq > 1 ? 4 / key : 0) ? (int)line : 0;
-    p.worth = second ? 0 : 1 + (unsigned)cost;
+    p.worth = 1 + (unsigned)cost;
     p.cut = p.line ? ((size_t)blocks * sizeof(Cut) + 255) / 256 * 256 : 0;
     p.ml = (size_t)p.line * 2 * rows * sizeof(float2);
     p.o = (size_t)p.line * 2 * rows * d.D * sizeof(float);
