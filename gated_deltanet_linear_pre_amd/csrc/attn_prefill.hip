@@ -26,7 +26,8 @@
 // Few rows over many keys (a chunk that goes on from a long cache) would leave most CUs idle.
 // The keys of all rows then form one line that is cut into equal parts, one a block, as in the
 // step: rows within one part are finished there, of rows that are cut each part leaves O, maximum
-// and sum in the workspace, and a second kernel joins them.  Whether that pays is said by line_us().
+// and sum in the workspace, and a second kernel joins them.  Whether that pays is said by line_us(), first
+// by the bounds that the host knows, then by the lengths on the device.
 //
 // Precision.  Scores, maxima, sums and O are fp32; 16-bit weights are rounded to the
 // io type for the product with V (half a step of each weight, of random sign: as much as
@@ -36,9 +37,10 @@
 // V that is not finite would turn 0 into NaN there, so it is made 0 in LDS in such
 // a tile, and the rows that see it become NaN in its channel at the end.
 //
-// Measured: 2048 tokens of 32 heads of 128, fp16, 54 us (635 TFLOP/s of what the mask leaves), 8192
-// tokens 0.59 ms (936); 8192 tokens of 16 heads of 256, bf16, 0.62 ms (882); chunks of
-// 391 tokens over caches of up to 32768 keys 219 us (725).
+// Measured: 2048 tokens of 32 heads of 128, fp16, 56 us (619 TFLOP/s of what the mask leaves), 8192
+// tokens 0.59 ms (930); 8192 tokens of 16 heads of 256, bf16, 0.63 ms (875); chunks of
+// 391 tokens over caches of up to 32768 keys 219 us (726).  fp32, 4096 tokens: 32 heads of 128 1.14 ms (120), 16
+// of 256 1.33 (103).
 #include "attn_device.h"
 #include "mfma_device.h"
 
@@ -770,9 +772,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttnDims d, PrefillArgs s)
 
 // What the line costs beside its keys, in us: ends of the parts and the join, more the more parts there are, and
 // the more of them hold ends of two rows.  Measured without and with it: 16 heads of 256, 64 tokens after
-// 1000 45 and 19 us, 300 after 300 31 and 22, 600 from their start 31 and 27, 900 40 and 42, 1500 60 and 84; 32 heads
-// of 128, 512 tokens 20 and 24, after 1500 49 and 42, 1024 30 and 48.  Of batches, 115 tokens after 3780 with five short
-// prompts, 20 heads of 192, 95 and 59; more blocks than are resident, 1475 tokens after 5788, 24 heads of 256, 415 and 307.
+// 1000 46 and 20 us, 300 after 300 31 and 23, 600 from their start 31 and 28, 900 41 and 43, 1500 61 and 84; 32 heads
+// of 128, 512 tokens 20 and 25, after 1500 50 and 42, 1024 31 and 49.  Of batches, 115 tokens after 3780 with five short
+// prompts, 20 heads of 192, 94 and 59; more blocks than are resident, 1475 tokens after 5788, 24 heads of 256, 422 and 318.
 double line_us(double full, double parts) { return 6.6 * (1 + parts + full) + 66 * full * full; }
 // and a key of a block alone on its CU
 double key_us(bool f32, int D) { return f32 ? 0.0006 * D : 0.006 + 0.000105 * D; }

@@ -6,7 +6,7 @@
 // product, and up to 8 waves of a block take as many such tiles over the same keys (a unit:
 // sequence, key-value head, those tiles), so that K and V come from memory once: bound by HBM
 // bandwidth.  (Tile after tile, 32 sequences of 8000 keys of 64 heads of 128 over one take 90 us, side by
-// side 54; 16 of 64 heads of 256 over two 90 and 70.)
+// side 56; 16 of 64 heads of 256 over two 90 and 69.)
 //
 // Work.  The keys of all units, in chunks of 64, form one line that is cut into equal
 // parts, one a block: every block finds its place by a prefix sum over kv_len, so the
@@ -25,14 +25,16 @@
 // operands and its V copied to LDS without registers, whose transposing reads give 4 keys of a channel a
 // lane (V through registers, and so 4 waves a CU at D = 256: 88 us for what takes 79).
 // Both are read once, so past the caches' order (83 us without for 76); not where several waves want the same
-// keys (54 us above, 73 so).
+// keys (56 us above, 73 so).
 //
 // Precision.  Scores, maxima, sums and O are fp32.  16-bit weights enter the product
 // with V in two parts of the matrix type (2^-16 of a weight at bf16, 2^-22 at fp16, or
 // 2^-25 of the largest): the matrix pipes have the time.
 //
 // Measured: one sequence of 99991 keys, 32 heads of 128 over 8, fp16, 71 us (5.8 TB/s); 64 sequences of up to
-// 20011 keys, 16 heads of 256 over 2, bf16, 79 us (5.2 TB/s); one of 701 keys 11 us.
+// 20011 keys, 16 heads of 256 over 2, bf16, 80 us (5.2 TB/s); one of 701 keys 11 us; fp32, 32 of 4001 keys, 32 heads
+// of 128 over 8, 162 us (6.5 TB/s).  Units of at most 64 keys, of which 2 waves at most have a tile, are slow:
+// 4096 sequences of 61 keys 545 us (2.1 TB/s).
 #include "attn_device.h"
 #include "mfma_device.h"
 
