@@ -1,19 +1,16 @@
 """A kernel that runs out of vector registers keeps some in scratch memory or in accumulation
 registers.  What brings them back are loads like any other: scratch loads may not land on
 an operand of a product in flight either, nor may loads into accumulation registers (the rule
-of tests/asm_hazards.py, which looks at LDS and global loads into vector registers).  Compiles every
-csrc/*.hip to assembly with the library's own flags (hipcc cross-compiles without a GPU)."""
-import glob
+of tests/asm_hazards.py, which looks at LDS and global loads into vector registers).  The assembly is that of
+tests/test_asm_hazards.py, every csrc/*.hip compiled with the library's own flags."""
 import os
 import re
-import subprocess
 
 import pytest
 
 from gated_deltanet_linear_pre_amd import build as B
 from tests import asm_hazards
-
-SOURCES = sorted(glob.glob(os.path.join(B.CSRC, "*.hip")))
+from tests.test_asm_hazards import SOURCES, _asm
 
 
 def loads_over_operands(asm_text, monkeypatch):
@@ -26,11 +23,7 @@ def loads_over_operands(asm_text, monkeypatch):
 @pytest.mark.skipif(not os.path.exists(B.HIPCC), reason="hipcc not installed")
 @pytest.mark.parametrize("src", SOURCES, ids=[os.path.basename(s) for s in SOURCES])
 def test_no_spill_overwrites_an_mfma_operand_in_flight(src, tmp_path, monkeypatch):
-    out = tmp_path / "a.s"
-    r = subprocess.run([B.HIPCC, *[f for f in B.CFLAGS if f != "-fPIC"], "--offload-device-only", "-S", src, "-o", str(out)],
-                       capture_output=True, text=True)
-    assert r.returncode == 0, r.stderr[-2000:]
-    found = loads_over_operands(out.read_text(), monkeypatch)
+    found = loads_over_operands(_asm(src, tmp_path), monkeypatch)
     assert not found, "\n".join(f"{f[:60]} line {n}: {ins} (MFMA at line {m})" for f, n, ins, m in found)
 
 

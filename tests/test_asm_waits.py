@@ -1,26 +1,19 @@
 """No kernel's vector-memory instruction reads a scalar register too soon after it was
-written (see tests/asm_waits.py).  Compiles every csrc/*.hip to assembly with the library's own
-flags (hipcc cross-compiles without a GPU)."""
-import glob
+written (see tests/asm_waits.py).  The assembly is that of
+tests/test_asm_hazards.py, every csrc/*.hip compiled with the library's own flags."""
 import os
-import subprocess
 
 import pytest
 
 from gated_deltanet_linear_pre_amd import build as B
 from tests.asm_waits import short_waits
-
-SOURCES = sorted(glob.glob(os.path.join(B.CSRC, "*.hip")))
+from tests.test_asm_hazards import SOURCES, _asm
 
 
 @pytest.mark.skipif(not os.path.exists(B.HIPCC), reason="hipcc not installed")
 @pytest.mark.parametrize("src", SOURCES, ids=[os.path.basename(s) for s in SOURCES])
 def test_no_load_reads_a_scalar_register_too_soon(src, tmp_path):
-    out = tmp_path / "a.s"
-    r = subprocess.run([B.HIPCC, *[f for f in B.CFLAGS if f != "-fPIC"], "--offload-device-only", "-S", src, "-o", str(out)],
-                       capture_output=True, text=True)
-    assert r.returncode == 0, r.stderr[-2000:]
-    found = short_waits(out.read_text())
+    found = short_waits(_asm(src, tmp_path))
     assert not found, f"{len(found)}\n" + "\n".join(f"{f[:60]} line {n}: {ins} (s{r} after {w} of {need})" for f, n, ins, r, w, need in found[:20])
 
 
